@@ -3,7 +3,9 @@
 The package is a thin ctypes binding over libengram.so: a C-ABI library of
 hand-written HIP kernels (hash, row gather + dequant, bf16 MFMA projection,
 the projection fused with the Q2_K row dequant, the MXFP8 projection of raw
-FP8 rows, and the gate) plus their composition.  Build the library with
+FP8 rows, and the gate) plus their composition, and the operators of a
+decoder layer's attention step (query/key norm and rotation, paged cache,
+paged attention, 4-bit projection).  Build the library with
 `python gram_hash_memory_amd/build.py`.  Importing the package without it,
 or with a library built from other sources than those beside it, raises
 ImportError; there is no CPU fallback.
@@ -18,4 +20,7 @@ from ._binding import (  # noqa: F401
     engram_project_mxfp8, engram_stage_mxfp8, engram_project_mxfp8_staged, engram_gate,
     engram_gate_layers, engram_workspace_bytes, engram_forward, engram_last_error,
     engram_build_id, BUILD_ID, engram_forward_noalloc, FORWARD_NOALLOC_MAX_BYTES,
+    ENGRAM_CACHE_BF16, ENGRAM_CACHE_MXFP8, MX_BLOCK, KVCache, engram_cache_write,
+    engram_cache_read, engram_qk_norm_rope, engram_paged_attention_workspace_bytes,
+    engram_paged_attention, engram_quantize_mxfp4, engram_project_mxfp4,
 )

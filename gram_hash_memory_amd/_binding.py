@@ -26,13 +26,17 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libengram.s
 
 ENGRAM_OK, ENGRAM_ERR_ARG, ENGRAM_ERR_UNSUPPORTED, ENGRAM_ERR_HIP = 0, 1, 2, 3
 ENGRAM_ROWS_Q2K, ENGRAM_ROWS_FP8_E4M3_E8M0 = 0, 1
+ENGRAM_CACHE_BF16, ENGRAM_CACHE_MXFP8 = 0, 1
+MX_BLOCK = 32
 HEAD_DIM, Q2K_ROW_BYTES, FP8_ROW_BYTES, FP8_SCALE_BYTES = 256, 84, 256, 8
 
 EXPORTS = ("engram_hash", "engram_history_update", "engram_rows", "engram_project", "engram_project_q2k",
            "engram_project_fp8", "engram_quantize_mxfp8", "engram_project_mxfp8",
            "engram_stage_mxfp8", "engram_project_mxfp8_staged", "engram_gate",
            "engram_gate_layers", "engram_workspace_bytes", "engram_forward", "engram_last_error",
-           "engram_build_id", "engram_forward_noalloc")
+           "engram_build_id", "engram_forward_noalloc", "engram_cache_write",
+           "engram_cache_read", "engram_qk_norm_rope", "engram_paged_attention_workspace_bytes",
+           "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python gram_hash_memory_amd/build.py`")
@@ -77,6 +81,12 @@ class _Layer(ctypes.Structure):
                 ("k_weight", c_void_p), ("wkv_mx", c_void_p), ("wkv_mx_scales", c_void_p)]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("fmt", c_int), ("pages", c_int32), ("kv_heads", c_int32),
+                ("page_size", c_int32), ("head_dim", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("k_scales", c_void_p), ("v_scales", c_void_p)]
+
+
 _P = ctypes.POINTER
 _lib.engram_hash.argtypes = [_P(_HashParams), _P(_Tokens), c_void_p, c_void_p]
 _lib.engram_history_update.argtypes = [_P(_Tokens), c_int32, c_void_p, c_void_p, c_void_p]
@@ -109,11 +119,29 @@ _lib.engram_forward.argtypes = [_P(_HashParams), _P(_Tokens), _P(_Layer), c_void
 _lib.engram_forward_noalloc.argtypes = [_P(_HashParams), _P(_Tokens), _P(_Layer), c_void_p,
                                         c_int32, c_int32, c_float, c_float, c_float, c_void_p,
                                         c_void_p]
+_lib.engram_cache_write.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                    c_int64, c_void_p, c_int32, c_void_p, c_void_p]
+_lib.engram_cache_read.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                   c_void_p]
+_lib.engram_qk_norm_rope.argtypes = [c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
+                                     c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int32,
+                                     c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p]
+_lib.engram_paged_attention_workspace_bytes.argtypes = [c_int32] * 5
+_lib.engram_paged_attention_workspace_bytes.restype = c_size_t
+_lib.engram_paged_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int32,
+                                        c_int32, c_int32, c_float, c_int32, c_void_p, c_void_p,
+                                        c_void_p, c_size_t, c_void_p, c_void_p]
+_lib.engram_quantize_mxfp4.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]
+_lib.engram_project_mxfp4.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                      c_int32, c_void_p]
 _lib.engram_last_error.restype = c_char_p
 for _name in ("engram_hash", "engram_history_update", "engram_rows", "engram_project", "engram_project_q2k",
               "engram_project_fp8", "engram_quantize_mxfp8", "engram_project_mxfp8",
               "engram_stage_mxfp8", "engram_project_mxfp8_staged", "engram_gate",
-              "engram_gate_layers", "engram_forward", "engram_forward_noalloc"):
+              "engram_gate_layers", "engram_forward", "engram_forward_noalloc",
+              "engram_cache_write", "engram_cache_read", "engram_qk_norm_rope",
+              "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4"):
     getattr(_lib, _name).restype = c_int
 
 
@@ -400,3 +428,143 @@ def engram_forward_noalloc(params: HashParams, tokens: Tokens, layers, h, hc: in
                                        int(hc), int(dim), float(eps), float(clamp),
                                        float(dot_scale), _dptr(bad_ids, torch.int32, 1, "bad_ids"),
                                        _stream(stream)))
+
+
+# ---------------------------------------------------------------- the attention step
+
+
+class KVCache:
+    """engram_kv_cache over GPU tensors (kept alive as long as this object).
+
+    k, v: [pages, kv_heads, page_size, head_dim], int16 bf16 bits or, for
+    ENGRAM_CACHE_MXFP8, uint8 e4m3fn codes with k_scales, v_scales uint8
+    [pages, kv_heads, page_size, head_dim / 32].
+    """
+
+    def __init__(self, fmt: int, k, v, k_scales=None, v_scales=None):
+        if fmt not in (ENGRAM_CACHE_BF16, ENGRAM_CACHE_MXFP8):
+            raise ValueError(f"unknown cache format {fmt}")
+        mx = fmt == ENGRAM_CACHE_MXFP8
+        if mx != (k_scales is not None) or mx != (v_scales is not None):
+            raise ValueError("an MXFP8 cache has k_scales and v_scales, a bf16 cache has none")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [pages, kv_heads, page_size, head_dim]")
+        dtype, n = (torch.uint8 if mx else torch.int16), k.numel()
+        self.fmt = fmt
+        self.pages, self.kv_heads, self.page_size, self.head_dim = (int(x) for x in k.shape)
+        scales = n // MX_BLOCK
+        self._keep = (k, v, k_scales, v_scales)
+        self.c = _KVCache(fmt, self.pages, self.kv_heads, self.page_size, self.head_dim,
+                          _dptr(k, dtype, n, "k"), _dptr(v, dtype, n, "v"),
+                          _dptr(k_scales, torch.uint8, scales, "k_scales"),
+                          _dptr(v_scales, torch.uint8, scales, "v_scales"))
+        self.address = ctypes.addressof(self.c)
+
+
+def _strided(t, dtype, dims: int, name: str):
+    """Device pointer of a GPU tensor whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
+    return t.data_ptr()
+
+
+def engram_cache_write(cache: KVCache, k, v, slots, bad_slots=None, stream=None) -> None:
+    """Keys and values int16 [T, kv_heads, head_dim] (bf16 bits; views with token and head
+    strides of multiples of 8) into the cache's places slots int64 [T]."""
+    T = int(k.shape[0])
+    want = (T, cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != want or tuple(v.shape) != want:
+        raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
+
+    def strides(x):      # a dimension of size 1 has no stride of its own; torch may report any
+        return (x.stride(0) if T > 1 else 0,
+                x.stride(1) if cache.kv_heads > 1 else cache.head_dim)
+    _check(_lib.engram_cache_write(
+        cache.address, _strided(k, torch.int16, 3, "k"), *strides(k),
+        _strided(v, torch.int16, 3, "v"), *strides(v),
+        _dptr(slots, torch.int64, T, "slots"), T, _dptr(bad_slots, torch.int32, 1, "bad_slots"),
+        _stream(stream)))
+
+
+def engram_cache_read(cache: KVCache, slots, k, v, bad_slots=None, stream=None) -> None:
+    """Places slots int64 [T] of the cache as bf16: k, v int16 [T, kv_heads, head_dim]."""
+    T = int(slots.numel())
+    n = T * cache.kv_heads * cache.head_dim
+    _check(_lib.engram_cache_read(
+        cache.address, _dptr(slots, torch.int64, T, "slots"), T, _dptr(k, torch.int16, n, "k"),
+        _dptr(v, torch.int16, n, "v"), _dptr(bad_slots, torch.int32, 1, "bad_slots"),
+        _stream(stream)))
+
+
+def engram_qk_norm_rope(qkv, q_heads: int, kv_heads: int, head_dim: int, q_weight, k_weight,
+                        eps: float, positions, inv_freq, interleaved: bool, q, k=None,
+                        cache: KVCache | None = None, slots=None, bad_slots=None,
+                        stream=None) -> None:
+    """Per-head RMS norm and rotation of the queries and keys in rows qkv int16 [T, width]
+    (a view with a row stride of a multiple of 8 will do): queries to q [T, q_heads,
+    head_dim], keys to k [T, kv_heads, head_dim] and / or, with the row's values, into the
+    cache's places slots int64 [T].  positions int32 [T], inv_freq float64 [rotary_dim / 2]."""
+    p = _strided(qkv, torch.int16, 2, "qkv")
+    T, width = qkv.shape
+    need = (q_heads + (kv_heads if cache is None else 2 * kv_heads)) * head_dim
+    if width < need:
+        raise ValueError(f"qkv has rows of {width} values, needs {need}")
+    # A single row has no stride of its own; torch may report any.
+    _check(_lib.engram_qk_norm_rope(
+        p, qkv.stride(0) if T > 1 else (need + 7) // 8 * 8, T, q_heads, kv_heads, head_dim,
+        _dptr(q_weight, torch.int16, head_dim, "q_weight"),
+        _dptr(k_weight, torch.int16, head_dim, "k_weight"), eps,
+        _dptr(positions, torch.int32, T, "positions"),
+        _dptr(inv_freq, torch.float64, 0, "inv_freq"), 2 * inv_freq.numel(), bool(interleaved),
+        _dptr(q, torch.int16, T * q_heads * head_dim, "q"),
+        _dptr(k, torch.int16, T * kv_heads * head_dim, "k"),
+        None if cache is None else cache.address, _dptr(slots, torch.int64, T, "slots"),
+        _dptr(bad_slots, torch.int32, 1, "bad_slots"), _stream(stream)))
+
+
+def engram_paged_attention_workspace_bytes(n_seqs: int, q_heads: int, kv_heads: int,
+                                           head_dim: int, max_len: int) -> int:
+    return int(_lib.engram_paged_attention_workspace_bytes(n_seqs, q_heads, kv_heads, head_dim,
+                                                           max_len))
+
+
+def engram_paged_attention(cache: KVCache, q, table, lens, max_len: int, scale: float, out,
+                           workspace=None, window: int = 0, lse=None, bad_pages=None,
+                           stream=None) -> None:
+    """Attention of one new token per sequence: q, out int16 [n_seqs, q_heads, head_dim],
+    table int32 [n_seqs, pages], lens int32 [n_seqs], lse float32 [n_seqs, q_heads]."""
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [n_seqs, q_heads, {cache.head_dim}], got {tuple(q.shape)}")
+    if table.dim() != 2 or table.shape[0] != q.shape[0]:
+        raise ValueError(f"table must be [n_seqs={q.shape[0]}, pages], got {tuple(table.shape)}")
+    n, heads, D = q.shape
+    width = int(table.shape[1])
+    _check(_lib.engram_paged_attention(
+        cache.address, _dptr(q, torch.int16, 0, "q"), _dptr(table, torch.int32, 0, "table"),
+        width, _dptr(lens, torch.int32, n, "lens"), n, heads, max_len, scale, window,
+        _dptr(out, torch.int16, n * heads * D, "out"), _dptr(lse, torch.float32, n * heads, "lse"),
+        _dptr(workspace, torch.uint8, 0, "workspace"),
+        0 if workspace is None else workspace.numel(),
+        _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
+
+
+def engram_quantize_mxfp4(w, N: int, K: int, codes, scales, stream=None) -> None:
+    """MXFP4 copy of bf16 w [N, K]: codes uint8 [N, K/2] (e2m1, even k low), scales uint8
+    [N, K/32] (e8m0)."""
+    _check(_lib.engram_quantize_mxfp4(_dptr(w, torch.int16, N * K, "w"), int(N), int(K),
+                                      _dptr(codes, torch.uint8, N * (K // 2), "codes"),
+                                      _dptr(scales, torch.uint8, N * (K // MX_BLOCK), "scales"),
+                                      _stream(stream)))
+
+
+def engram_project_mxfp4(x, codes, scales, out, T: int, K: int, N: int, stream=None) -> None:
+    """out [T, N] = x [T, K] (bf16 bits) x the MXFP4 weight [N, K]^T."""
+    _check(_lib.engram_project_mxfp4(_dptr(x, torch.int16, T * K, "x"),
+                                     _dptr(codes, torch.uint8, N * (K // 2), "codes"),
+                                     _dptr(scales, torch.uint8, N * (K // MX_BLOCK), "scales"),
+                                     _dptr(out, torch.int16, T * N, "out"), int(T), int(K),
+                                     int(N), _stream(stream)))

@@ -630,3 +630,244 @@ engram_status engram_forward_noalloc(const engram_hash_params *params,
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- the attention step
+
+namespace {
+
+bool head_dim_ok(int32_t D) { return D >= 32 && D <= ENGRAM_MAX_ATTN_HEAD_DIM && D % 32 == 0; }
+
+#define REQUIRE_HEAD_DIM(D)                                                                  \
+  REQUIRE_SUP(head_dim_ok(D), "head_dim=%d must be a multiple of %d in 32..%d", D,           \
+              ENGRAM_MX_BLOCK, ENGRAM_MAX_ATTN_HEAD_DIM)
+
+// A launch of 256-thread workgroups: the grid's threads are counted in 32 bits.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;
+
+engram_status check_cache(const engram_kv_cache *c, engram::CacheView *view) {
+  REQUIRE(c, "engram_kv_cache is NULL");
+  REQUIRE(c->fmt == ENGRAM_CACHE_BF16 || c->fmt == ENGRAM_CACHE_MXFP8,
+          "unknown cache format %d", int(c->fmt));
+  REQUIRE(c->pages >= 1 && c->kv_heads >= 1, "pages=%d and kv_heads=%d must be positive",
+          c->pages, c->kv_heads);
+  REQUIRE_HEAD_DIM(c->head_dim);
+  REQUIRE_SUP(c->page_size >= 8 && c->page_size <= ENGRAM_MAX_PAGE_SIZE &&
+                  (c->page_size & (c->page_size - 1)) == 0,
+              "page_size=%d must be a power of two in 8..%d", c->page_size, ENGRAM_MAX_PAGE_SIZE);
+  REQUIRE(c->k && c->v && aligned(c->k, 16) && aligned(c->v, 16),
+          "the cache's k or v is NULL or not 16-byte aligned");
+  if (c->fmt == ENGRAM_CACHE_MXFP8) {
+    REQUIRE(c->k_scales && c->v_scales && aligned(c->k_scales, 16) && aligned(c->v_scales, 16),
+            "the cache's k_scales or v_scales is NULL or not 16-byte aligned");
+  } else {
+    REQUIRE(!c->k_scales && !c->v_scales, "a bf16 cache has no scales");
+  }
+  *view = engram::CacheView{c->k, c->v, c->k_scales, c->v_scales,
+                            int64_t(c->pages) * c->page_size, c->pages, c->kv_heads, c->head_dim,
+                            __builtin_ctz(unsigned(c->page_size))};
+  return ENGRAM_OK;
+}
+
+engram_status check_slots(const int64_t *slots, const int32_t *bad_slots) {
+  REQUIRE(slots && aligned(slots, 8), "slots is NULL or not 8-byte aligned");
+  REQUIRE(!bad_slots || aligned(bad_slots, 4), "bad_slots misaligned");
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+engram_status engram_cache_write(const engram_kv_cache *cache, const uint16_t *k,
+                                 int64_t k_token_stride, int64_t k_head_stride,
+                                 const uint16_t *v, int64_t v_token_stride,
+                                 int64_t v_head_stride, const int64_t *slots, int32_t T,
+                                 int32_t *bad_slots, hipStream_t stream) {
+  engram::CacheView c;
+  engram_status st = check_cache(cache, &c);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  if (T == 0) return ENGRAM_OK;
+  REQUIRE(k && v && aligned(k, 16) && aligned(v, 16), "k or v is NULL or not 16-byte aligned");
+  REQUIRE(k_token_stride >= 0 && v_token_stride >= 0 && k_token_stride % 8 == 0 &&
+              v_token_stride % 8 == 0,
+          "token strides must be multiples of 8");
+  REQUIRE(k_head_stride >= c.head_dim && v_head_stride >= c.head_dim && k_head_stride % 8 == 0 &&
+              v_head_stride % 8 == 0,
+          "head strides must be multiples of 8 and at least head_dim=%d", c.head_dim);
+  if ((st = check_slots(slots, bad_slots)) != ENGRAM_OK) return st;
+  REQUIRE_SUP(engram::cache_move_blocks(c.kv_heads, c.head_dim, T) <= kMaxBlocks,
+              "T=%d tokens of %d heads are too many for one call", T, c.kv_heads);
+  return hip_status(engram::launch_cache_write(c, k, k_token_stride, k_head_stride, v,
+                                               v_token_stride, v_head_stride, slots, T, bad_slots,
+                                               stream),
+                    "engram_cache_write launch");
+}
+
+engram_status engram_cache_read(const engram_kv_cache *cache, const int64_t *slots, int32_t T,
+                                uint16_t *k, uint16_t *v, int32_t *bad_slots,
+                                hipStream_t stream) {
+  engram::CacheView c;
+  engram_status st = check_cache(cache, &c);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  if (T == 0) return ENGRAM_OK;
+  REQUIRE(k && v && aligned(k, 16) && aligned(v, 16), "k or v is NULL or not 16-byte aligned");
+  if ((st = check_slots(slots, bad_slots)) != ENGRAM_OK) return st;
+  REQUIRE_SUP(engram::cache_move_blocks(c.kv_heads, c.head_dim, T) <= kMaxBlocks,
+              "T=%d tokens of %d heads are too many for one call", T, c.kv_heads);
+  return hip_status(engram::launch_cache_read(c, slots, T, k, v, bad_slots, stream),
+                    "engram_cache_read launch");
+}
+
+engram_status engram_qk_norm_rope(const uint16_t *qkv, int64_t qkv_token_stride, int32_t T,
+                                  int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                  const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                                  const int32_t *positions, const double *inv_freq,
+                                  int32_t rotary_dim, int32_t interleaved, uint16_t *q,
+                                  uint16_t *k, const engram_kv_cache *cache,
+                                  const int64_t *slots, int32_t *bad_slots, hipStream_t stream) {
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  REQUIRE(q_heads >= 1 && kv_heads >= 1, "q_heads=%d and kv_heads=%d must be positive", q_heads,
+          kv_heads);
+  REQUIRE_HEAD_DIM(head_dim);
+  REQUIRE_SUP(rotary_dim >= 16 && rotary_dim <= head_dim && rotary_dim % 16 == 0,
+              "rotary_dim=%d must be a multiple of 16 in 16..head_dim=%d", rotary_dim, head_dim);
+  REQUIRE(eps >= 0.f, "eps must be >= 0");
+  REQUIRE_SUP((int64_t(q_heads) + 2 * int64_t(kv_heads)) * head_dim <= kInt32Max,
+              "a row of %d + 2 * %d heads is too long", q_heads, kv_heads);
+  engram::QkRope a{};
+  engram_status st;
+  if (cache) {
+    if ((st = check_cache(cache, &a.cache)) != ENGRAM_OK) return st;
+    REQUIRE(a.cache.kv_heads == kv_heads && a.cache.head_dim == head_dim,
+            "the cache has %d heads of %d, the row %d of %d", a.cache.kv_heads, a.cache.head_dim,
+            kv_heads, head_dim);
+  }
+  const int64_t used = (int64_t(q_heads) + (cache ? 2 : 1) * int64_t(kv_heads)) * head_dim;
+  REQUIRE(qkv_token_stride >= used && qkv_token_stride % 8 == 0,
+          "qkv_token_stride=%lld must be a multiple of 8 and at least %lld",
+          (long long)qkv_token_stride, (long long)used);
+  if (T == 0) return ENGRAM_OK;
+  REQUIRE(qkv && q && aligned(qkv, 16) && aligned(q, 16),
+          "qkv or q is NULL or not 16-byte aligned");
+  REQUIRE(k || cache, "the keys need k or a cache to go to");
+  REQUIRE(!k || aligned(k, 16), "k must be 16-byte aligned");
+  REQUIRE(q_weight && k_weight && aligned(q_weight, 16) && aligned(k_weight, 16),
+          "q_weight or k_weight is NULL or not 16-byte aligned");
+  REQUIRE(positions && aligned(positions, 4), "positions is NULL or misaligned");
+  REQUIRE(inv_freq && aligned(inv_freq, 8), "inv_freq is NULL or misaligned");
+  if (cache) {
+    if ((st = check_slots(slots, bad_slots)) != ENGRAM_OK) return st;
+  } else {
+    REQUIRE(!slots && !bad_slots, "slots and bad_slots go with a cache");
+  }
+  a.qkv = qkv;
+  a.token_stride = qkv_token_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.q = q;
+  a.k = k;
+  a.slots = slots;
+  a.bad_slots = bad_slots;
+  a.T = T;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.rotary_dim = rotary_dim;
+  a.eps = eps;
+  const int64_t blocks = engram::qk_rope_plan(&a);
+  REQUIRE_SUP(blocks <= kMaxBlocks, "T=%d tokens of %d heads are too many for one call", T,
+              q_heads + kv_heads);
+  return hip_status(engram::launch_qk_norm_rope(a, interleaved != 0, blocks, stream),
+                    "engram_qk_norm_rope launch");
+}
+
+size_t engram_paged_attention_workspace_bytes(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
+                                              int32_t head_dim, int32_t max_len) {
+  if (n_seqs <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 ||
+      !head_dim_ok(head_dim) || max_len <= 0)
+    return 0;
+  return size_t(engram::paged_attention_workspace(n_seqs, q_heads, kv_heads, head_dim, max_len));
+}
+
+engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_t *q,
+                                     const int32_t *table, int32_t table_width,
+                                     const int32_t *lens, int32_t n_seqs, int32_t q_heads,
+                                     int32_t max_len, float scale, int32_t window, uint16_t *out,
+                                     float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t *bad_pages, hipStream_t stream) {
+  engram::PagedAttention a{};
+  engram_status st = check_cache(cache, &a.cache);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(n_seqs >= 0 && max_len >= 0 && window >= 0 && table_width >= 0,
+          "n_seqs=%d, max_len=%d, window=%d and table_width=%d must not be negative", n_seqs,
+          max_len, window, table_width);
+  REQUIRE(q_heads >= 1 && q_heads % a.cache.kv_heads == 0,
+          "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, a.cache.kv_heads);
+  REQUIRE(scale == scale && scale - scale == 0.f, "scale must be finite");
+  if (n_seqs == 0) return ENGRAM_OK;
+  REQUIRE(q && out && aligned(q, 16) && aligned(out, 16),
+          "q or out is NULL or not 16-byte aligned");
+  REQUIRE(lens && aligned(lens, 4), "lens is NULL or misaligned");
+  REQUIRE((table && aligned(table, 4)) || table_width == 0, "table is NULL or misaligned");
+  REQUIRE(!lse || aligned(lse, 4), "lse misaligned");
+  REQUIRE(!bad_pages || aligned(bad_pages, 4), "bad_pages misaligned");
+  const size_t need = engram_paged_attention_workspace_bytes(n_seqs, q_heads, a.cache.kv_heads,
+                                                             a.cache.head_dim, max_len);
+  REQUIRE(need == 0 || (workspace && aligned(workspace, 256)),
+          "workspace is NULL or not 256-byte aligned");
+  REQUIRE(workspace_bytes >= need, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
+  a.q = q;
+  a.table = table;
+  a.lens = lens;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.bad_pages = bad_pages;
+  a.table_width = table_width;
+  a.n_seqs = n_seqs;
+  a.q_heads = q_heads;
+  a.max_len = max_len;
+  a.window = window;
+  a.scale = scale;
+  REQUIRE_SUP(int64_t(n_seqs) * q_heads <= kMaxBlocks, "n_seqs=%d of %d heads are too many",
+              n_seqs, q_heads);
+  return hip_status(engram::launch_paged_attention(a, stream), "engram_paged_attention launch");
+}
+
+engram_status engram_quantize_mxfp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,
+                                    uint8_t *scales, hipStream_t stream) {
+  REQUIRE(N >= 0, "N=%d < 0", N);
+  REQUIRE(K > 0 && K % 32 == 0, "K=%d must be a positive multiple of 32", K);
+  REQUIRE_SUP(int64_t(N) * (K / 32) <= kMaxBlocks * 256, "a weight of %d x %d is too large", N, K);
+  if (N == 0) return ENGRAM_OK;
+  REQUIRE(w && codes && scales, "w, codes or scales is NULL");
+  REQUIRE(aligned(w, 16) && aligned(codes, 16), "w and codes must be 16-byte aligned");
+  return hip_status(engram::launch_quantize_fp4(w, N, K, codes, scales, stream),
+                    "engram_quantize_mxfp4 launch");
+}
+
+engram_status engram_project_mxfp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                                   uint16_t *out, int32_t T, int32_t K, int32_t N,
+                                   hipStream_t stream) {
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  REQUIRE(K > 0 && K % 32 == 0, "K=%d must be a positive multiple of 32", K);
+  REQUIRE(N > 0, "N=%d must be positive", N);
+  REQUIRE_SUP(int64_t(N) * (K / 2) <= ENGRAM_MX_MAX_WEIGHT_BYTES,
+              "MXFP4 weight of %d x %d values exceeds %lld bytes", N, K,
+              (long long)ENGRAM_MX_MAX_WEIGHT_BYTES);
+  REQUIRE_SUP(int64_t(T) * K * 2 <= ENGRAM_MX_MAX_WEIGHT_BYTES,
+              "x of %d x %d values exceeds %lld bytes", T, K,
+              (long long)ENGRAM_MX_MAX_WEIGHT_BYTES);
+  if (T == 0) return ENGRAM_OK;
+  REQUIRE(x && codes && out && aligned(x, 16) && aligned(codes, 16) && aligned(out, 16),
+          "x, codes or out is NULL or not 16-byte aligned");
+  REQUIRE(scales, "scales is NULL");
+  return hip_status(engram::launch_project_fp4(x, codes, scales, out, T, K, N, stream),
+                    "engram_project_mxfp4 launch");
+}
+
+}  // extern "C"

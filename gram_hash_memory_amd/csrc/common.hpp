@@ -144,4 +144,63 @@ hipError_t launch_gate(float *h, const uint16_t *kv, const uint16_t *qw, const u
                        const uint8_t *mask, int32_t T, int32_t hc, int32_t dim, float eps,
                        float clamp, float dot_scale, hipStream_t stream);
 
+// ---------------------------------------------------------------- the attention step
+
+// A paged cache as a kernel argument; k_scales is NULL for bf16.
+struct CacheView {
+  void *k, *v;
+  uint8_t *k_scales, *v_scales;
+  int64_t slots;                 // pages * page_size
+  int32_t pages, kv_heads, head_dim, page_shift;
+};
+
+// Workgroups of a cache write or read of T tokens (kv_cache.hip).
+int64_t cache_move_blocks(int32_t kv_heads, int32_t head_dim, int64_t T);
+hipError_t launch_cache_write(const CacheView &c, const uint16_t *k, int64_t k_token,
+                              int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head,
+                              const int64_t *slots, int32_t T, int32_t *bad_slots,
+                              hipStream_t stream);
+hipError_t launch_cache_read(const CacheView &c, const int64_t *slots, int32_t T, uint16_t *k,
+                             uint16_t *v, int32_t *bad_slots, hipStream_t stream);
+
+struct QkRope {
+  const uint16_t *qkv;
+  int64_t token_stride;
+  const uint16_t *q_weight, *k_weight;
+  const int32_t *positions;
+  const double *inv_freq;
+  uint16_t *q, *k;               // k NULL: into the cache only
+  CacheView cache;               // cache.k NULL: none
+  const int64_t *slots;
+  int32_t *bad_slots;
+  int32_t T, q_heads, kv_heads, head_dim, rotary_dim;
+  float eps;
+  // From qk_rope_plan: the heads a token has here (the values' ones with a
+  // cache), and how many of them a wave takes.
+  int32_t heads, heads_per_wave, waves_per_token;
+};
+int64_t qk_rope_plan(QkRope *a);            // workgroups
+hipError_t launch_qk_norm_rope(const QkRope &a, bool interleaved, int64_t blocks,
+                               hipStream_t stream);
+
+struct PagedAttention {
+  CacheView cache;
+  const uint16_t *q;
+  const int32_t *table, *lens;
+  uint16_t *out;
+  float *lse;
+  void *workspace;
+  int32_t *bad_pages;
+  int32_t table_width, n_seqs, q_heads, max_len, window;
+  float scale;
+};
+int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
+                                  int32_t head_dim, int32_t max_len);
+hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream);
+
+hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,
+                               uint8_t *scales, hipStream_t stream);
+hipError_t launch_project_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                              uint16_t *out, int32_t T, int32_t K, int32_t N, hipStream_t stream);
+
 }  // namespace engram

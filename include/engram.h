@@ -85,6 +85,8 @@ typedef enum engram_row_format ENGRAM_ENUM_BASE {
 #define ENGRAM_MAX_COLS 64         /* (max_ngram - 1) * n_heads per layer          */
 #define ENGRAM_MAX_HC 8            /* hyper-connection streams                     */
 #define ENGRAM_MAX_DIM 8192        /* hidden size                                  */
+#define ENGRAM_MAX_ATTN_HEAD_DIM 256  /* attention head size: a multiple of 32      */
+#define ENGRAM_MX_BLOCK 32         /* values per e8m0 scale                        */
 
 /* Hash-table metadata of all engram layers ([vLLM] EngramLayout and
  * compute_hash_multipliers; the spark page ships them as checkpoint
@@ -453,6 +455,166 @@ ENGRAM_API engram_status engram_forward_noalloc(const engram_hash_params *params
                                                 int32_t hc, int32_t dim, float eps, float clamp,
                                                 float dot_scale, int32_t *bad_ids,
                                                 hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The decoder layer's attention step, for programs that stream tokens through
+ * a layer beside the Engram forward: per-head norms and rotation of queries
+ * and keys, a paged key-value cache in bf16 or in 8 bits, attention of one new
+ * token per sequence over it, and the projection of few tokens by a 4-bit
+ * weight.  Conventions as above.
+ * ------------------------------------------------------------------------ */
+
+typedef enum engram_cache_format ENGRAM_ENUM_BASE {
+  ENGRAM_CACHE_BF16 = 0,
+  ENGRAM_CACHE_MXFP8 = 1           /* e4m3fn codes, one e8m0 byte per 32 values   */
+} engram_cache_format;
+
+/* A paged cache.  DEVICE pointers, 16-byte aligned.
+ *   k, v [pages][kv_heads][page_size][head_dim]: bf16, or e4m3fn codes.
+ *   k_scales, v_scales [pages][kv_heads][page_size][head_dim/32] e8m0 (byte b
+ *        means 2^(b-127), for b in 1..254): MXFP8 only, NULL for bf16.
+ * Slot s of the cache is place s % page_size of page s / page_size.
+ * head_dim: a multiple of 32, 32..ENGRAM_MAX_ATTN_HEAD_DIM.  page_size: a
+ * power of two, 8..ENGRAM_MAX_PAGE_SIZE.
+ * The MXFP8 scale of 32 consecutive values is the smallest power of two 2^e,
+ * e >= -95, that brings their largest finite magnitude to 448 or below (byte
+ * 127 where it is 0); codes round to nearest even.  (A weight's copy from
+ * engram_quantize_mxfp8 saturates values above 448 instead: keys and values
+ * have no second pass that would notice.)  Infinities and NaN become NaN.
+ */
+#define ENGRAM_MAX_PAGE_SIZE 4096
+typedef struct engram_kv_cache {
+  engram_cache_format fmt;
+  int32_t pages;               /* >= 1                                            */
+  int32_t kv_heads;            /* >= 1                                            */
+  int32_t page_size;
+  int32_t head_dim;
+  void *k;
+  void *v;
+  uint8_t *k_scales;
+  uint8_t *v_scales;
+} engram_kv_cache;
+
+/* Keys and values of T tokens into the cache, quantised there for MXFP8.
+ *   k, v DEVICE bf16: head h of token t starts at t * token_stride + h *
+ *   head_stride (in values, multiples of 8, head_stride >= head_dim or the
+ *   heads of a token would overlap).  slots DEVICE int64 [T]: token t's
+ *   slot; -1 marks a padding token, which is not written; any other slot
+ *   outside the cache is not written either and counted in bad_slots (DEVICE
+ *   int32, nullable).  Two tokens with one slot: the caller's mistake, which
+ *   of their values stay is open.  k and v must not lie in the cache.
+ */
+ENGRAM_API engram_status engram_cache_write(const engram_kv_cache *cache, const uint16_t *k,
+                                            int64_t k_token_stride, int64_t k_head_stride,
+                                            const uint16_t *v, int64_t v_token_stride,
+                                            int64_t v_head_stride, const int64_t *slots,
+                                            int32_t T, int32_t *bad_slots, hipStream_t stream);
+
+/* Keys and values of T slots out of the cache, in bf16.
+ *   slots DEVICE int64 [T], in any order, repeated or not; -1 and slots outside
+ *   the cache give zeros, the latter counted in bad_slots (nullable).
+ *   k, v DEVICE bf16 [T][kv_heads][head_dim], fully overwritten.  An MXFP8
+ *   value is code * 2^(byte - 127) rounded to bf16 (exact but for values
+ *   below bf16's normal range).
+ */
+ENGRAM_API engram_status engram_cache_read(const engram_kv_cache *cache, const int64_t *slots,
+                                           int32_t T, uint16_t *k, uint16_t *v,
+                                           int32_t *bad_slots, hipStream_t stream);
+
+/* Norm and rotation of queries and keys, out of rows of a QKV projection.
+ *   qkv DEVICE bf16: row t starts at t * qkv_token_stride (values, a multiple
+ *   of 8): q_heads queries, kv_heads keys and (needed with a cache) kv_heads
+ *   values of head_dim each.  For each head x of queries or keys, in fp32:
+ *     y_i = x_i / sqrt(mean(x^2) + eps) * weight_i;
+ *     then dims 0..rotary_dim-1 are rotated in pairs (a, b), pair i by the
+ *     angle positions[t] * inv_freq[i] (formed and reduced in fp64):
+ *     a' = a cos - b sin, b' = b cos + a sin; pair i is dims (i, i +
+ *     rotary_dim/2), or with interleaved != 0 dims (2i, 2i + 1).  Dims from
+ *     rotary_dim on are normed only.  Each result is rounded to bf16 once.
+ *   q_weight, k_weight DEVICE bf16 [head_dim].  positions DEVICE int32 [T].
+ *   inv_freq DEVICE double [rotary_dim/2].  rotary_dim: a multiple of 16 in
+ *   16..head_dim.
+ *   q DEVICE bf16 [T][q_heads][head_dim].  Keys go to k DEVICE bf16
+ *   [T][kv_heads][head_dim], or, with cache and slots, into the cache (as
+ *   engram_cache_write would put the bf16 results, the row's values with
+ *   them; slots and bad_slots as there), or both; one of them is needed.
+ *   Outputs must not overlap the inputs.
+ */
+ENGRAM_API engram_status engram_qk_norm_rope(const uint16_t *qkv, int64_t qkv_token_stride,
+                                             int32_t T, int32_t q_heads, int32_t kv_heads,
+                                             int32_t head_dim, const uint16_t *q_weight,
+                                             const uint16_t *k_weight, float eps,
+                                             const int32_t *positions, const double *inv_freq,
+                                             int32_t rotary_dim, int32_t interleaved,
+                                             uint16_t *q, uint16_t *k,
+                                             const engram_kv_cache *cache, const int64_t *slots,
+                                             int32_t *bad_slots, hipStream_t stream);
+
+/* Bytes of device workspace engram_paged_attention needs: the partial results
+ * of sequences that are split over their length (0: none is).  A window needs
+ * no more. */
+ENGRAM_API size_t engram_paged_attention_workspace_bytes(int32_t n_seqs, int32_t q_heads,
+                                                         int32_t kv_heads, int32_t head_dim,
+                                                         int32_t max_len);
+
+/* Attention of one new token per sequence over the paged cache.
+ *   q DEVICE bf16 [n_seqs][q_heads][head_dim]; q_heads a multiple of the
+ *   cache's kv_heads: query head h attends to key-value head h / (q_heads /
+ *   kv_heads).  Place p of sequence s is place p % page_size of page table[s *
+ *   table_width + p / page_size] (DEVICE int32).  lens DEVICE int32 [n_seqs]:
+ *   the sequence's length, its newest token included; a length below 0 counts
+ *   as 0, one above max_len or table_width * page_size as the smaller of these.
+ *   The places seen are max(0, len - window) .. len - 1 (window 0: all).
+ *   Entries of the table for other places are not used, and what the cache
+ *   holds there may be anything, NaN included.  The places of a page outside
+ *   the cache are not seen; bad_pages (DEVICE int32, nullable) is incremented
+ *   at least once if there is one.
+ *     out = sum_p exp(scale q.k_p) v_p / sum_p exp(scale q.k_p), in bf16;
+ *     lse (DEVICE fp32 [n_seqs][q_heads], nullable) = log sum_p exp(scale q.k_p).
+ *   Where nothing is seen out is 0 and lse -infinity.  Scores, softmax
+ *   statistics and sums are held in fp32; the weights exp(.) are rounded to
+ *   bf16 for the matrix cores, and their sum is that of the fp32 ones.
+ *   Sequences are split over their length where there are too few of them to
+ *   fill the GPU; the parts are joined in a fixed order, so results do not
+ *   depend on timing.
+ *   workspace DEVICE, 256-byte aligned, at least
+ *   engram_paged_attention_workspace_bytes(...) bytes (NULL if that is 0);
+ *   its contents are scratch.
+ */
+ENGRAM_API engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_t *q,
+                                                const int32_t *table, int32_t table_width,
+                                                const int32_t *lens, int32_t n_seqs,
+                                                int32_t q_heads, int32_t max_len, float scale,
+                                                int32_t window, uint16_t *out, float *lse,
+                                                void *workspace, size_t workspace_bytes,
+                                                int32_t *bad_pages, hipStream_t stream);
+
+/* MXFP4 copy of a bf16 weight, for engram_project_mxfp4 (OCP MX v1.0, E2M1).
+ *   w DEVICE bf16 [N][K], K % 32 == 0; codes DEVICE [N][K/2], 16-byte aligned:
+ *   value k of a row is bits 4*(k%2) .. + 3 of byte k/2; scales DEVICE
+ *   [N][K/32] e8m0.  Per 32 consecutive k: scale byte = floor(log2 amax) - 2 +
+ *   127 clamped to 0..254 (127 when amax = 0); each code is w / 2^(byte-127)
+ *   saturated to +-6 and rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6,
+ *   ties to the even code.  Inf/NaN inputs are not supported.
+ */
+ENGRAM_API engram_status engram_quantize_mxfp4(const uint16_t *w, int32_t N, int32_t K,
+                                               uint8_t *codes, uint8_t *scales,
+                                               hipStream_t stream);
+
+/* The product of few tokens with a 4-bit weight: out[t][n] = bf16(sum_k x[t][k]
+ * * e2m1(codes[n][k]) * 2^(scales[n][k/32] - 127)).
+ *   x DEVICE bf16 [T][K], codes DEVICE [N][K/2] and scales DEVICE [N][K/32] as
+ *   engram_quantize_mxfp4 lays them out (scale bytes 0..254; codes 16-byte
+ *   aligned, scales any alignment), out DEVICE bf16 [T][N], fully overwritten;
+ *   K % 32 == 0.  The weight's values are exact in bf16; products accumulate
+ *   in fp32 on the matrix cores, in a fixed order, and each output is rounded
+ *   once.  Made for up to some 128 tokens, where reading the weight is what
+ *   takes time; more tokens are right but run in tiles that each read it again.
+ *   Limits: N * K/2 and T * K * 2 <= ENGRAM_MX_MAX_WEIGHT_BYTES.
+ */
+ENGRAM_API engram_status engram_project_mxfp4(const uint16_t *x, const uint8_t *codes,
+                                              const uint8_t *scales, uint16_t *out, int32_t T,
+                                              int32_t K, int32_t N, hipStream_t stream);
 
 /* Message for the calling thread's last non-OK status ("" if none). */
 ENGRAM_API const char *engram_last_error(void);
