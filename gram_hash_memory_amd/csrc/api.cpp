@@ -643,6 +643,7 @@ bool head_dim_ok(int32_t D) { return D >= 32 && D <= ENGRAM_MAX_ATTN_HEAD_DIM &&
 
 // A launch of 256-thread workgroups: the grid's threads are counted in 32 bits.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;
+constexpr int64_t kMaxAttnBlocks = kMaxBlocks / 2;       // up to 512 threads each
 
 engram_status check_cache(const engram_kv_cache *c, engram::CacheView *view) {
   REQUIRE(c, "engram_kv_cache is NULL");
@@ -833,8 +834,9 @@ engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_
   a.max_len = max_len;
   a.window = window;
   a.scale = scale;
-  REQUIRE_SUP(int64_t(n_seqs) * q_heads <= kMaxBlocks, "n_seqs=%d of %d heads are too many",
-              n_seqs, q_heads);
+  REQUIRE_SUP(engram::paged_attention_blocks(a) <= kMaxAttnBlocks,
+              "n_seqs=%d of %d heads over max_len=%d are too many for one call", n_seqs, q_heads,
+              max_len);
   return hip_status(engram::launch_paged_attention(a, stream), "engram_paged_attention launch");
 }
 
