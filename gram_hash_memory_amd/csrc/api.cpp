@@ -643,7 +643,6 @@ bool head_dim_ok(int32_t D) { return D >= 32 && D <= ENGRAM_MAX_ATTN_HEAD_DIM &&
 
 // A launch of 256-thread workgroups: the grid's threads are counted in 32 bits.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;
-constexpr int64_t kMaxAttnBlocks = kMaxBlocks / 2;       // up to 512 threads each
 
 engram_status check_cache(const engram_kv_cache *c, engram::CacheView *view) {
   REQUIRE(c, "engram_kv_cache is NULL");
@@ -806,6 +805,7 @@ engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_
   REQUIRE(n_seqs >= 0 && max_len >= 0 && window >= 0 && table_width >= 0,
           "n_seqs=%d, max_len=%d, window=%d and table_width=%d must not be negative", n_seqs,
           max_len, window, table_width);
+  REQUIRE_SUP(max_len <= 1 << 30, "max_len=%d exceeds %d", max_len, 1 << 30);
   REQUIRE(q_heads >= 1 && q_heads % a.cache.kv_heads == 0,
           "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, a.cache.kv_heads);
   REQUIRE(scale == scale && scale - scale == 0.f, "scale must be finite");
@@ -834,7 +834,9 @@ engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_
   a.max_len = max_len;
   a.window = window;
   a.scale = scale;
-  REQUIRE_SUP(engram::paged_attention_blocks(a) <= kMaxAttnBlocks,
+  REQUIRE_SUP(int64_t(n_seqs) * q_heads <= kMaxBlocks &&
+                  engram::paged_attention_units(n_seqs, q_heads, a.cache.kv_heads, max_len) <=
+                      kInt32Max - kMaxBlocks,
               "n_seqs=%d of %d heads over max_len=%d are too many for one call", n_seqs, q_heads,
               max_len);
   return hip_status(engram::launch_paged_attention(a, stream), "engram_paged_attention launch");

@@ -32,68 +32,55 @@ namespace {
 using kvc::row_index;
 
 constexpr int kTile = 32;                  // places a wave takes at a time
-constexpr int kMaxChunk = 4096;            // places of a workgroup: their pages are held in LDS
+constexpr int kW = 4;                      // waves of a workgroup
+constexpr int kUnit = kTile * kW;          // places the work is dealt out by
+constexpr int kMaxChunk = 4096;            // places whose pages are held in LDS at a time
 constexpr int kMinPage = 8;
 constexpr int kHeadBlock = 32;             // query heads of a workgroup
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- the plan
 
-// The grid is laid out for sequences of max_len places (the host does not know
-// their lengths); workgroups past a sequence's end leave at once.
-constexpr int64_t kWantedBlocks = 2048;
-constexpr int64_t kMinChunk = 256;
-constexpr int64_t kMaxSplits = 256;
-constexpr int kSingleSpan = 512;
+// The host does not know the lengths, so the workgroups deal out the work
+// themselves: the units of all (sequence, key-value head) pairs, in that order,
+// are cut into as many equal runs as there are workgroups.  A run's pieces of
+// pairs that it does not hold whole (two at most: its first and its last) go
+// to the workspace, and join_kernel adds a pair's pieces in order.  Pairs of
+// few units (direct_units) take one workgroup each, and there is nothing to join.
+constexpr int64_t kBlocks = 256;
+
+// Up to 4 units (512 places) the join costs more than it saves (one stream of
+// 300 places: 8.3 us against 11.3 us); up to 8 where the pairs fill the CUs on
+// their own (64 streams of up to 1000: 36.9 against 46 us; one stream of 1000:
+// 13.9 against 11.3 us).
+inline int64_t direct_units(int64_t pairs) { return pairs >= kBlocks ? 8 : 4; }
+
+inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
 struct Plan {
-  int head_blocks, chunk, splits, waves;   // chunk: a multiple of kTile * waves
+  int64_t pairs, units, blocks;            // units: of one pair at most
+  int head_blocks;
+  bool direct;
 };
 
-inline int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
-Plan plan_for(int n_seqs, int q_heads, int kv_heads, int head_dim, int span) {
+Plan plan_for(int n_seqs, int q_heads, int kv_heads, int max_len) {
   Plan p{};
-  const int group = q_heads / kv_heads;
-  p.head_blocks = (group + kHeadBlock - 1) / kHeadBlock;
-  const int64_t pairs = int64_t(n_seqs) * kv_heads * p.head_blocks;
-  if (span <= kSingleSpan) {
-    // 8 waves where their results fit 56 KB of LDS for the join (and a wave 256 registers).
-    p.waves = head_dim / 32 * std::min(16, group) <= 64 ? 8 : 4;
-    p.chunk = int(round_up(std::max(span, 1), kTile * p.waves));
-    p.splits = 1;
-    return p;
-  }
-  p.waves = 4;
-  const int64_t even = (int64_t(span) * pairs + kWantedBlocks - 1) / kWantedBlocks;
-  const int64_t most = (int64_t(span) + kMaxSplits - 1) / kMaxSplits;
-  p.chunk = int(std::min<int64_t>(
-      kMaxChunk, round_up(std::max({even, most, kMinChunk}), kTile * p.waves)));
-  p.splits = int((int64_t(span) + p.chunk - 1) / p.chunk);
+  p.head_blocks = int(ceil_div(q_heads / kv_heads, kHeadBlock));
+  p.pairs = int64_t(n_seqs) * kv_heads * p.head_blocks;
+  p.units = std::max<int64_t>(1, ceil_div(max_len, kUnit));
+  p.direct = p.units <= direct_units(p.pairs);
+  p.blocks = p.direct ? p.pairs : std::min(kBlocks, p.pairs * p.units);
   return p;
 }
 
-// The plan of a call: that of its window's places, in no more parts than the
-// workspace (sized without the window) has room for.
-Plan plan_for(const PagedAttention &a) {
-  const int hkv = a.cache.kv_heads;
-  const Plan whole = plan_for(a.n_seqs, a.q_heads, hkv, a.cache.head_dim, a.max_len);
-  if (a.window <= 0 || int64_t(a.window) + kTile - 1 >= a.max_len) return whole;
-  const int span = a.window + kTile - 1;   // the first place is rounded down to a tile
-  Plan p = plan_for(a.n_seqs, a.q_heads, hkv, a.cache.head_dim, span);
-  if (p.splits > whole.splits) {
-    p.chunk = int(round_up((int64_t(span) + whole.splits - 1) / whole.splits, kTile * p.waves));
-    p.splits = int((int64_t(span) + p.chunk - 1) / p.chunk);
-  }
-  return p;
-}
-
-// ---------------------------------------------------------------- the kernel
-
+// The workspace: of each run two pieces [heads of a block][head_dim] and their
+// (m, sum), then the units before each sequence and their number in a run.
 struct Split {
-  float *o;                // [n_seqs * q_heads][splits][head_dim], relative to 2^m
-  float2 *ml;              // [n_seqs * q_heads][splits]: m (of base 2), the sum
-  int chunk, splits, head_blocks;
+  float *o;
+  float2 *ml;
+  int32_t *before;         // [n_seqs + 1], [n_seqs + 1] units of a run
+  int32_t blocks, head_blocks, block_heads;
+  bool direct;
 };
 
 // How the head_dim = 32 * kDb dimensions fall to 16 lanes: pieces of 16, 8, 4,
@@ -162,14 +149,16 @@ __device__ __forceinline__ float column_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// The places of a sequence that are seen.
+// The places of a sequence that are seen, from its start rounded down to a tile.
 struct Seen {
-  int start, len;
+  int start, len, base, units;
 };
 __device__ __forceinline__ Seen seen_of(const PagedAttention &a, int64_t s) {
   const int64_t room = int64_t(a.table_width) << a.cache.page_shift;
   const int len = int(min(int64_t(min(max(a.lens[s], 0), a.max_len)), room));
-  return {a.window > 0 ? max(0, len - a.window) : 0, len};
+  const int start = a.window > 0 ? max(0, len - a.window) : 0;
+  const int base = start / kTile * kTile;
+  return {start, len, base, int((int64_t(len) - base + kUnit - 1) / kUnit)};
 }
 
 // 32 places' keys and values in a lane's registers, as they lie in the cache.
@@ -182,8 +171,57 @@ struct Held {
   uint32_t vs[8][kN];
 };
 
-template <int kDb, bool kMx, int kHt, int kW>
-__global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attention_kernel(
+// Where a run starts: this workgroup's first unit is unit `local` of the
+// sequence s's pairs.  Writes the workspace's `before` too (workgroup 0).
+struct Run {
+  int s, local, left;
+};
+__device__ __forceinline__ Run run_of(const PagedAttention &a, const Split &sp, int pairs) {
+  __shared__ int wave_lds[kW], run_lds[2];
+  const int per_thread = (a.n_seqs + 64 * kW - 1) / (64 * kW);
+  const int s0 = threadIdx.x * per_thread, s1 = min(a.n_seqs, s0 + per_thread);
+  int mine = 0;
+  for (int s = s0; s < s1; ++s) mine += seen_of(a, s).units * pairs;
+  int upto = mine;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) {
+    const int y = __shfl_up(upto, x);
+    if (int(threadIdx.x & 63) >= x) upto += y;
+  }
+  if ((threadIdx.x & 63) == 63) wave_lds[threadIdx.x >> 6] = upto;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w == int(threadIdx.x >> 6)) upto += total;
+    total += wave_lds[w];
+  }
+  int before = upto - mine;
+  const int per = max(1, (total + sp.blocks - 1) / sp.blocks);
+  const int64_t u0 = int64_t(blockIdx.x) * per;
+  if (u0 >= before && u0 < upto) {
+    int s = s0, local = int(u0) - before;
+    for (;; ++s) {
+      const int n = seen_of(a, s).units * pairs;
+      if (local < n) break;
+      local -= n;
+    }
+    run_lds[0] = s, run_lds[1] = local;
+  }
+  if (blockIdx.x == 0) {
+    for (int s = s0; s < s1; ++s) {
+      sp.before[s] = before;
+      before += seen_of(a, s).units * pairs;
+    }
+    if (threadIdx.x == 0) sp.before[a.n_seqs] = total, sp.before[a.n_seqs + 1] = per;
+  }
+  __syncthreads();
+  if (u0 >= total) return {0, 0, 0};
+  return {run_lds[0], run_lds[1], int(min(int64_t(per), total - u0))};
+}
+
+template <int kDb, bool kMx, int kHt>
+__global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attention_kernel(
     PagedAttention a, Split sp) {
   constexpr int D = 32 * kDb, kRowBytes = kMx ? D : 2 * D, kAcc = D / 16;
   using P = Pieces<kDb>;
@@ -194,42 +232,37 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attentio
   const CacheView &c = a.cache;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t id = blockIdx.x;
-  const int split = int(id % sp.splits);
-  id /= sp.splits;
-  const int hb = int(id % sp.head_blocks);
-  id /= sp.head_blocks;
-  const int kvh = int(id % c.kv_heads);
-  const int64_t s = id / c.kv_heads;
-  const int group = a.q_heads / c.kv_heads;
-  const int heads = min(16 * kHt, group - hb * kHeadBlock);   // here; kHt = 1 only for up to 16
-  const int64_t row0 = s * a.q_heads + kvh * group + hb * kHeadBlock;
-
-  const Seen seen = seen_of(a, s);
-  const int base = seen.start / kTile * kTile;
-  const int64_t c0_wide = int64_t(base) + int64_t(split) * sp.chunk;
-  if (c0_wide >= seen.len && sp.splits > 1) return;
-  const int c0 = int(min(c0_wide, int64_t(seen.len)));
-  const int c1 = int(min(int64_t(seen.len), int64_t(c0) + sp.chunk));
-  const int tiles = (c1 - c0 + kTile - 1) / kTile;
-
-  // The pages of these places.
+  const int group = a.q_heads / c.kv_heads, pairs = c.kv_heads * sp.head_blocks;
   const int mask = (1 << c.page_shift) - 1;
-  const int page0 = c0 >> c.page_shift;
-  const int pages = tiles == 0 ? 0 : int((int64_t(c0) + tiles * kTile - 1) >> c.page_shift) - page0 + 1;
-  bool bad = false;
-  for (int e = threadIdx.x; e < pages; e += 64 * kW) {
-    const int64_t first = int64_t(page0 + e) << c.page_shift;
-    int64_t row = -1;
-    if (first < c1 && first + mask >= seen.start) {
-      const int page = a.table[s * a.table_width + page0 + e];
-      if (page >= 0 && page < c.pages) row = (int64_t(page) * c.kv_heads + kvh) << c.page_shift;
-      else bad = true;
-    }
-    page_lds[e] = row;
+  const float to_log2 = a.scale * kLog2e;
+
+  Run run{int(blockIdx.x / pairs), 0, 1};
+  if (!sp.direct) run = run_of(a, sp, pairs);
+  run.s = __builtin_amdgcn_readfirstlane(run.s);
+  run.local = __builtin_amdgcn_readfirstlane(run.local);
+  run.left = __builtin_amdgcn_readfirstlane(run.left);
+  for (int piece = 0; run.left > 0; ++piece) {
+  const int s = run.s;
+  const Seen seen = seen_of(a, s);
+  if (seen.units == 0 && !sp.direct) {
+    ++run.s;
+    --piece;
+    continue;
   }
-  if (bad && kvh == 0 && hb == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
-  const bool any_bad = __syncthreads_or(bad);
+  // Units first .. first + count - 1 of the pair.
+  const int pair = sp.direct ? int(blockIdx.x % pairs) : run.local / seen.units;
+  const int first_unit = sp.direct ? 0 : run.local - pair * seen.units;
+  const int count = sp.direct ? seen.units : min(seen.units - first_unit, run.left);
+  const bool whole_pair = count == seen.units;
+  run.left -= sp.direct ? 1 : count;
+  run.local += count;
+  if (run.local == seen.units * pairs) ++run.s, run.local = 0;
+
+  const int kvh = pair / sp.head_blocks, hb = pair - kvh * sp.head_blocks;
+  const int heads = min(16 * kHt, group - hb * kHeadBlock);   // here; kHt = 1 only for up to 16
+  const int64_t row0 = int64_t(s) * a.q_heads + kvh * group + hb * kHeadBlock;
+  const int begin = seen.base + first_unit * kUnit;
+  const int end = int(min(int64_t(seen.len), int64_t(begin) + int64_t(count) * kUnit));
 
   // Query heads as B operands: lane l holds 8 dimensions of head l % 16 a step.
   // In the 8-bit format a lane's 16 bytes of K are two steps.
@@ -239,11 +272,42 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attentio
 #pragma unroll
     for (int kk = 0; kk < kDb; ++kk) {
       const int d = kMx && (kk | 1) < kDb ? 64 * (kk / 2) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
-      u32x4 v{};
-      if (16 * t + col < heads)
-        v = *reinterpret_cast<const u32x4 *>(a.q + (row0 + 16 * t + col) * D + d);
-      q[t][kk] = __builtin_bit_cast(bf16x8, v);
+      // Columns past the last head repeat it; nothing reads their results.
+      q[t][kk] = __builtin_bit_cast(
+          bf16x8, *reinterpret_cast<const u32x4 *>(
+                      a.q + (row0 + min(16 * t + col, heads - 1)) * D + d));
     }
+
+  float m[kHt], l[kHt];
+  f32x4 o[kHt][kAcc];
+#pragma unroll
+  for (int t = 0; t < kHt; ++t) {
+    m[t] = -INFINITY, l[t] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kAcc; ++n) o[t][n] = f32x4{};
+  }
+
+  for (int c0 = begin; c0 < end; c0 += kMaxChunk) {
+  const int c1 = int(min(int64_t(end), int64_t(c0) + kMaxChunk));
+  const int tiles = (c1 - c0 + kTile - 1) / kTile;
+
+  // The pages of these places.
+  const int page0 = c0 >> c.page_shift;
+  const int pages = int((int64_t(c0) + tiles * kTile - 1) >> c.page_shift) - page0 + 1;
+  bool bad = false;
+  if (c0 > begin) __syncthreads();             // the pages before are in use up to here
+  for (int e = threadIdx.x; e < pages; e += 64 * kW) {
+    const int64_t first = int64_t(page0 + e) << c.page_shift;
+    int64_t row = -1;
+    if (first < c1 && first + mask >= seen.start) {
+      const int page = a.table[int64_t(s) * a.table_width + page0 + e];
+      if (page >= 0 && page < c.pages) row = (int64_t(page) * c.kv_heads + kvh) << c.page_shift;
+      else bad = true;
+    }
+    page_lds[e] = row;
+  }
+  if (bad && pair == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
+  const bool any_bad = __syncthreads_or(bad);
 
   Held<kDb, kMx> held;
   auto row_of = [&](int p) {
@@ -293,137 +357,132 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attentio
     }
   };
 
-  const float to_log2 = a.scale * kLog2e;
-  float m[kHt], l[kHt];
-  f32x4 o[kHt][kAcc];
-#pragma unroll
-  for (int t = 0; t < kHt; ++t) {
-    m[t] = -INFINITY, l[t] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kAcc; ++n) o[t][n] = f32x4{};
-  }
-
-  int tile = wave;
-  if (tile < tiles) {
+  // The loads are issued without a condition (the last ones for nothing, from
+  // the cache): a wave then waits for no more of them than it needs.
+  if (wave < tiles) {
+    int tile = wave;
     load_k(tile);
+    __builtin_amdgcn_sched_barrier(0);
     load_v(tile);
-  }
-  while (tile < tiles) {
-    const int p0 = c0 + kTile * tile;
-    f32x4 z[kHt][2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int t = 0; t < kHt; ++t) z[t][u] = f32x4{};
-#pragma unroll
-      for (int kk = 0; kk < kDb; ++kk) {
-        bf16x8 f;
-        if constexpr (kMx) {
-          const uint32_t *w = &held.k[u][2 * kk];
-          const float sc = __uint_as_float(held.ks[u][kk / 2] << 23);
-          f = as_frag(mx_pair(w[0], sc, false), mx_pair(w[0], sc, true), mx_pair(w[1], sc, false),
-                      mx_pair(w[1], sc, true));
-        } else {
-          const uint32_t *w = &held.k[u][4 * kk];
-          f = as_frag(w[0], w[1], w[2], w[3]);
-        }
-#pragma unroll
-        for (int t = 0; t < kHt; ++t)
-          z[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][kk], z[t][u], 0, 0, 0);
-      }
-    }
-    const int next = tile + kW;
-    load_k(min(next, tiles - 1));              // the last time for nothing, from the cache
-
-    // Bits 4 u + r: place 16 u + 4 g + r of the tile is seen.
-    const bool whole = !any_bad && p0 >= seen.start && p0 + kTile <= seen.len;
-    uint32_t shown = 0xFF;
-    if (!whole) {
-      shown = 0;
+    do {
+      const int next = min(tile + kW, tiles - 1);
+      const int p0 = c0 + kTile * tile;
+      f32x4 z[kHt][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int p = p0 + 16 * u + 4 * g;
-        const bool page = page_lds[(p >> c.page_shift) - page0] >= 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (page && p + r >= seen.start && p + r < seen.len) shown |= 1u << (4 * u + r);
-      }
+        for (int t = 0; t < kHt; ++t) z[t][u] = f32x4{};
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!(shown >> j & 1)) {
+        for (int kk = 0; kk < kDb; ++kk) {
+          bf16x8 f;
+          if constexpr (kMx) {
+            const uint32_t *w = &held.k[u][2 * kk];
+            const float sc = __uint_as_float(held.ks[u][kk / 2] << 23);
+            f = as_frag(mx_pair(w[0], sc, false), mx_pair(w[0], sc, true), mx_pair(w[1], sc, false),
+                        mx_pair(w[1], sc, true));
+          } else {
+            const uint32_t *w = &held.k[u][4 * kk];
+            f = as_frag(w[0], w[1], w[2], w[3]);
+          }
 #pragma unroll
-          for (int i = 0; i < int(sizeof(held.v[0]) / 4); ++i) held.v[j][i] = 0;
-#pragma unroll
-          for (int i = 0; i < P::kN; ++i) held.vs[j][i] = 127;
+          for (int t = 0; t < kHt; ++t)
+            z[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][kk], z[t][u], 0, 0, 0);
         }
-    }
-
-    bf16x8 w[kHt];                             // the weights, as B operands
-#pragma unroll
-    for (int t = 0; t < kHt; ++t) {
-      float e[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = z[t][j / 4][j % 4] * to_log2;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load_k(next);
+      __builtin_amdgcn_sched_barrier(0);
+      // Bits 4 u + r: place 16 u + 4 g + r of the tile is seen.  The values of
+      // others, which may be anything, count as 0 (times a scale that is finite).
+      const bool whole = !any_bad && p0 >= seen.start && p0 + kTile <= seen.len;
+      uint32_t shown = 0xFF;
       if (!whole) {
+        shown = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = shown >> j & 1 ? e[j] : -INFINITY;
+        for (int u = 0; u < 2; ++u) {
+          const int p = p0 + 16 * u + 4 * g;
+          const bool page = page_lds[(p >> c.page_shift) - page0] >= 0;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (page && p + r >= seen.start && p + r < seen.len) shown |= 1u << (4 * u + r);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < int(sizeof(held.v[0]) / 4); ++i)
+            held.v[j][i] = shown >> j & 1 ? held.v[j][i] : 0;
       }
-      float top = e[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) top = fmaxf(top, e[j]);
-      top = column_max(top);
-      if (__any(top > m[t])) {                 // rarely after the first tiles
-        const float mn = fmaxf(m[t], top);
-        const float keep = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        l[t] *= keep;
-#pragma unroll
-        for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
-      }
-      const float ms = m[t] == -INFINITY ? 0.0f : m[t];
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = __builtin_amdgcn_exp2f(e[j] - ms);
-        sum += e[j];
-      }
-      l[t] += sum;
-      // Rounded to bf16 for the matrix cores; the sum is of the fp32 ones.
-      w[t] = as_frag(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                     pack_bf16x2(e[6], e[7]));
-    }
 
-    each_piece<P::kN>([&](auto piece) {
-      constexpr int wd = P::width(piece.value), first = P::base(piece.value);
+      bf16x8 w[kHt];                             // the weights, as B operands
 #pragma unroll
-      for (int i = 0; i < wd / 2; ++i) {
-        uint32_t x[8];                   // dimensions 2 i, 2 i + 1 of the lane's 8 places
+      for (int t = 0; t < kHt; ++t) {
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = z[t][j / 4][j % 4] * to_log2;
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = shown >> j & 1 ? e[j] : -INFINITY;
+        }
+        float top = e[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, e[j]);
+        top = column_max(top);
+        if (__any(top > m[t])) {                 // rarely after the first tiles
+          const float mn = fmaxf(m[t], top);
+          const float keep = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+          m[t] = mn;
+          l[t] *= keep;
+#pragma unroll
+          for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
+        }
+        const float ms = m[t] == -INFINITY ? 0.0f : m[t];
+        float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if constexpr (kMx)
-            x[j] = mx_pair(held.v[j][first / 64 + i / 2],
-                           __uint_as_float(held.vs[j][piece.value] << 23), i & 1);
-          else
-            x[j] = held.v[j][first / 32 + i];
+          e[j] = __builtin_amdgcn_exp2f(e[j] - ms);
+          sum += e[j];
         }
-        const bf16x8 even = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u),
-                                    __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
-                                    __builtin_amdgcn_perm(x[5], x[4], 0x05040100u),
-                                    __builtin_amdgcn_perm(x[7], x[6], 0x05040100u));
-        const bf16x8 odd = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u),
-                                   __builtin_amdgcn_perm(x[3], x[2], 0x07060302u),
-                                   __builtin_amdgcn_perm(x[5], x[4], 0x07060302u),
-                                   __builtin_amdgcn_perm(x[7], x[6], 0x07060302u));
-        const int n = first / 16 + 2 * i;
-#pragma unroll
-        for (int t = 0; t < kHt; ++t) {
-          o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, w[t], o[t][n], 0, 0, 0);
-          o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, w[t], o[t][n + 1], 0, 0, 0);
-        }
+        l[t] += sum;
+        // Rounded to bf16 for the matrix cores; the sum is of the fp32 ones.
+        w[t] = as_frag(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                       pack_bf16x2(e[6], e[7]));
       }
-    });
-    tile = next;
-    if (tile < tiles) load_v(tile);
+
+      each_piece<P::kN>([&](auto piece) {
+        constexpr int wd = P::width(piece.value), first = P::base(piece.value);
+#pragma unroll
+        for (int i = 0; i < wd / 2; ++i) {
+          uint32_t x[8];                   // dimensions 2 i, 2 i + 1 of the lane's 8 places
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if constexpr (kMx)
+              x[j] = mx_pair(held.v[j][first / 64 + i / 2],
+                             __uint_as_float(min(held.vs[j][piece.value], 254u) << 23), i & 1);
+            else
+              x[j] = held.v[j][first / 32 + i];
+          }
+          const bf16x8 even = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u),
+                                      __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
+                                      __builtin_amdgcn_perm(x[5], x[4], 0x05040100u),
+                                      __builtin_amdgcn_perm(x[7], x[6], 0x05040100u));
+          const bf16x8 odd = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u),
+                                     __builtin_amdgcn_perm(x[3], x[2], 0x07060302u),
+                                     __builtin_amdgcn_perm(x[5], x[4], 0x07060302u),
+                                     __builtin_amdgcn_perm(x[7], x[6], 0x07060302u));
+          const int n = first / 16 + 2 * i;
+#pragma unroll
+          for (int t = 0; t < kHt; ++t) {
+            o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, w[t], o[t][n], 0, 0, 0);
+            o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, w[t], o[t][n + 1], 0, 0, 0);
+          }
+        }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      load_v(next);
+      __builtin_amdgcn_sched_barrier(0);
+    } while ((tile += kW) < tiles);
+  }
+
   }
 
   // The waves' results joined by wave 0, in wave order.
@@ -462,10 +521,11 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attentio
         o[t][n] += o_lds[((x - 1) * kAcc + n) * 4 * here + g * here + col] * keep;
     }
     const int64_t row = row0 + 16 * t + col;
-    const bool last = sp.splits == 1;
-    const float inv = !last ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    // A run's first piece, or a later one (the run's last) that it does not hold whole.
+    const int64_t part = (2 * int64_t(blockIdx.x) + (piece > 0)) * sp.block_heads + 16 * t + col;
+    const float inv = !whole_pair ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
     if (g == 0) {
-      if (!last) sp.ml[row * sp.splits + split] = float2{top, sum};
+      if (!whole_pair) sp.ml[part] = float2{top, sum};
       else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
     each_piece<P::kN>([&](auto piece) {
@@ -473,53 +533,69 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 8 ? 1 : 2) void paged_attentio
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int d = first + wd * (4 * g + r);
-        if (last) {
+        if (whole_pair) {
           uint16_t *dst = a.out + row * D + d;
 #pragma unroll
           for (int i = 0; i < wd / 2; ++i)
             reinterpret_cast<uint32_t *>(dst)[i] = pack_bf16x2(
                 o[t][first / 16 + 2 * i][r] * inv, o[t][first / 16 + 2 * i + 1][r] * inv);
         } else {
-          float *dst = sp.o + (row * sp.splits + split) * D + d;
+          float *dst = sp.o + part * D + d;
 #pragma unroll
           for (int i = 0; i < wd; ++i) dst[i] = o[t][first / 16 + i][r];
         }
       }
     });
   }
+  }
 }
 
-// The parts of a sequence's chunks to its result, in the chunks' order: one
-// workgroup per (sequence, query head), D / 4 lanes a part.
+// A pair's pieces to its result, in order: one workgroup per (sequence, query
+// head), D / 4 lanes a piece.
 constexpr int kJoinThreads = 256;
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Split sp) {
   __shared__ f32x4 part_lds[kJoinThreads];
   __shared__ float top_lds[kJoinThreads / 64], sum_lds[kJoinThreads / 64];
   const int D = a.cache.head_dim, lanes = D / 4;
   const int64_t row = blockIdx.x;
-  const Seen seen = seen_of(a, row / a.q_heads);
-  const int base = seen.start / kTile * kTile;
-  const int parts = int((int64_t(seen.len) - base + sp.chunk - 1) / sp.chunk);
-  const float2 *ml = sp.ml + row * sp.splits;
+  const int s = int(row / a.q_heads), h = int(row - int64_t(s) * a.q_heads);
+  const int group = a.q_heads / a.cache.kv_heads, kvh = h / group, in_group = h - kvh * group;
+  const int hb = in_group / kHeadBlock, pair = kvh * sp.head_blocks + hb;
+  const int first = sp.before[s], per = sp.before[a.n_seqs + 1];
+  const int units = (sp.before[s + 1] - first) / (a.cache.kv_heads * sp.head_blocks);
+  const int u0 = first + pair * units, u1 = u0 + units;
+  const int r0 = u0 / per;
+  const int parts = units == 0 ? 0 : (u1 - 1) / per - r0 + 1;
+  if (parts == 1) return;                          // its run has written the result
+  // The first run holds the pair's beginning: as its first piece, or its last.
+  const int64_t at0 = int64_t(in_group - hb * kHeadBlock);
+  auto part_of = [&](int i) {
+    return (2 * int64_t(r0 + i) + (i == 0 && int64_t(r0) * per < u0)) * sp.block_heads + at0;
+  };
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float top = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads) top = fmaxf(top, ml[i].x);
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) top = fmaxf(top, sp.ml[part_of(i)].x);
   for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
   if (lane == 0) top_lds[wave] = top;
   __syncthreads();
   for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, top_lds[w]);
   const float ms = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads)
-    sum += ml[i].y * __builtin_amdgcn_exp2f(ml[i].x - ms);
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+    const float2 ml = sp.ml[part_of(i)];
+    sum += ml.y * __builtin_amdgcn_exp2f(ml.x - ms);
+  }
   for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
   if (lane == 0) sum_lds[wave] = sum;
 
   const int rows = kJoinThreads / lanes, mine = threadIdx.x / lanes, at = threadIdx.x % lanes;
   f32x4 o{};
   if (mine < rows) {
-    const f32x4 *src = reinterpret_cast<const f32x4 *>(sp.o + row * sp.splits * D) + at;
-    for (int i = mine; i < parts; i += rows) o += src[int64_t(i) * lanes] * __builtin_amdgcn_exp2f(ml[i].x - ms);
+    const f32x4 *src = reinterpret_cast<const f32x4 *>(sp.o) + at;
+    for (int i = mine; i < parts; i += rows) {
+      const int64_t part = part_of(i);
+      o += src[part * lanes] * __builtin_amdgcn_exp2f(sp.ml[part].x - ms);
+    }
     part_lds[threadIdx.x] = o;
   }
   __syncthreads();
@@ -534,66 +610,65 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Sp
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
-template <int kDb, bool kMx, int kHt, int kW>
-hipError_t launch(const PagedAttention &a, const Plan &p, const Split &sp, hipStream_t stream) {
-  const int group = a.q_heads / a.cache.kv_heads;
-  const unsigned lds = unsigned((kW - 1) * (2 * kDb) * 4 * std::min(16, group) * sizeof(f32x4));
-  const int64_t blocks = int64_t(a.n_seqs) * a.cache.kv_heads * p.head_blocks * p.splits;
-  hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, kHt, kW>), dim3(unsigned(blocks)),
-                     dim3(64 * kW), lds, stream, a, sp);
-  return hipGetLastError();
-}
-
 template <int kDb, bool kMx>
-hipError_t by_heads(const PagedAttention &a, const Plan &p, const Split &sp, hipStream_t stream) {
-  const bool two = a.q_heads / a.cache.kv_heads > 16;
-  if (p.waves == 8) {
-    if constexpr (kDb <= 4)
-      if (two) return launch<kDb, kMx, 2, 8>(a, p, sp, stream);
-    return launch<kDb, kMx, 1, 8>(a, p, sp, stream);
-  }
-  return two ? launch<kDb, kMx, 2, 4>(a, p, sp, stream) : launch<kDb, kMx, 1, 4>(a, p, sp, stream);
+void by_heads(const PagedAttention &a, const Split &sp, hipStream_t stream) {
+  const unsigned lds = unsigned((kW - 1) * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
+  const dim3 grid(sp.blocks), block(64 * kW);
+  if (sp.block_heads > 16)
+    hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, 2>), grid, block, lds, stream, a, sp);
+  else
+    hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, 1>), grid, block, lds, stream, a, sp);
 }
 
 template <int kDb>
-hipError_t by_format(const PagedAttention &a, const Plan &p, const Split &sp, hipStream_t stream) {
-  return a.cache.k_scales ? by_heads<kDb, true>(a, p, sp, stream)
-                          : by_heads<kDb, false>(a, p, sp, stream);
+void by_format(const PagedAttention &a, const Split &sp, hipStream_t stream) {
+  if (a.cache.k_scales) by_heads<kDb, true>(a, sp, stream);
+  else by_heads<kDb, false>(a, sp, stream);
 }
+
+inline int block_heads(int q_heads, int kv_heads) { return std::min(kHeadBlock, q_heads / kv_heads); }
 
 }  // namespace
 
-int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
-                                  int32_t head_dim, int32_t max_len) {
-  const Plan p = plan_for(n_seqs, q_heads, kv_heads, head_dim, max_len);
-  if (p.splits == 1) return 0;
-  return int64_t(n_seqs) * q_heads * p.splits * (head_dim + 2) * int64_t(sizeof(float));
+int64_t paged_attention_units(int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len) {
+  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len);
+  return p.pairs * p.units;
 }
 
-int64_t paged_attention_blocks(const PagedAttention &a) {
-  const Plan p = plan_for(a);
-  return std::max(int64_t(a.n_seqs) * a.cache.kv_heads * p.head_blocks * p.splits,
-                  int64_t(a.n_seqs) * a.q_heads);
+int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
+                                  int32_t head_dim, int32_t max_len) {
+  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len);
+  if (p.direct) return 0;
+  const int64_t parts = 2 * p.blocks * block_heads(q_heads, kv_heads);
+  return (parts * (head_dim + 2) + n_seqs + 2) * int64_t(sizeof(float));
 }
 
 hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream) {
-  const Plan p = plan_for(a);
-  const int64_t parts = int64_t(a.n_seqs) * a.q_heads * p.splits;
-  float *ws = static_cast<float *>(a.workspace);
-  const Split sp{ws, reinterpret_cast<float2 *>(ws + parts * a.cache.head_dim), p.chunk, p.splits,
-                 p.head_blocks};
-  hipError_t err;
-  switch (a.cache.head_dim / 32) {
-    case 1: err = by_format<1>(a, p, sp, stream); break;
-    case 2: err = by_format<2>(a, p, sp, stream); break;
-    case 3: err = by_format<3>(a, p, sp, stream); break;
-    case 4: err = by_format<4>(a, p, sp, stream); break;
-    case 5: err = by_format<5>(a, p, sp, stream); break;
-    case 6: err = by_format<6>(a, p, sp, stream); break;
-    case 7: err = by_format<7>(a, p, sp, stream); break;
-    default: err = by_format<8>(a, p, sp, stream);
+  const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
+  const Plan p = plan_for(a.n_seqs, a.q_heads, hkv, a.max_len);
+  Split sp{};
+  sp.blocks = int32_t(p.blocks);
+  sp.head_blocks = p.head_blocks;
+  sp.block_heads = block_heads(a.q_heads, hkv);
+  sp.direct = p.direct;
+  if (!p.direct) {
+    const int64_t parts = 2 * p.blocks * sp.block_heads;
+    sp.o = static_cast<float *>(a.workspace);
+    sp.ml = reinterpret_cast<float2 *>(sp.o + parts * D);
+    sp.before = reinterpret_cast<int32_t *>(sp.ml + parts);
   }
-  if (err != hipSuccess || p.splits == 1) return err;
+  switch (D / 32) {
+    case 1: by_format<1>(a, sp, stream); break;
+    case 2: by_format<2>(a, sp, stream); break;
+    case 3: by_format<3>(a, sp, stream); break;
+    case 4: by_format<4>(a, sp, stream); break;
+    case 5: by_format<5>(a, sp, stream); break;
+    case 6: by_format<6>(a, sp, stream); break;
+    case 7: by_format<7>(a, sp, stream); break;
+    default: by_format<8>(a, sp, stream);
+  }
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.direct) return err;
   hipLaunchKernelGGL(join_kernel, dim3(unsigned(int64_t(a.n_seqs) * a.q_heads)),
                      dim3(kJoinThreads), 0, stream, a, sp);
   return hipGetLastError();

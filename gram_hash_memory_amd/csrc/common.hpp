@@ -196,7 +196,8 @@ struct PagedAttention {
 };
 int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
                                   int32_t head_dim, int32_t max_len);
-int64_t paged_attention_blocks(const PagedAttention &a);     // the larger grid's
+// Units of work of a call at most (counted in 32 bits).
+int64_t paged_attention_units(int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len);
 hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream);
 
 hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,
