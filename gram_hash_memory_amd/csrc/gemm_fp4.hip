@@ -2,9 +2,20 @@
 //
 //   out[t][n] = bf16(sum_k x[t][k] * e2m1(code[n][k]) * 2^(scale[n][k/32] - 127))
 //
-// The plain kernel: one wave per output column, a lane a block of 32 k at a
-// time, the lanes' sums added at the end.
-#include "common.hpp"
+// Bound by reading the weight once, and for many tokens of a small weight by
+// pulling x through every CU's vector cache.  v_mfma_f32_16x16x32_bf16 with
+// the weight as A, which wants 8 neighbouring k of a column in each lane group
+// g = lane / 16: 4 bytes of codes.  A lane reads 16 bytes instead, a block of 32
+// k of its column, the 4 lane groups 4 neighbouring blocks; 4 lane swaps then
+// leave lane group g with dword g of each of the 4 blocks, and 3 more with
+// their scales.  (Taking a lane's 4 dwords as 4 steps as they lie needs no
+// swaps, but x in pieces of 16 bytes 64 apart: 53 us instead of XX at 64 tokens,
+// 6144 x 20480.)  One v_cvt_scalef32_pk_bf16_fp4 makes two scaled bf16 values.
+// Weights and x go from memory to registers, the former two steps of 128 k
+// ahead, the latter one.
+#include <algorithm>
+
+#include "gemm_common.hpp"
 
 namespace engram {
 namespace {
@@ -57,33 +68,259 @@ __global__ __launch_bounds__(kThreads) void quantize_fp4_kernel(const uint16_t *
   scales[b] = uint8_t(byte);
 }
 
-__device__ __forceinline__ float e2m1_to_float(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float a = e ? __uint_as_float((e + 126u) << 23 | m << 22) : 0.5f * float(m);
-  return c & 8u ? -a : a;
+// ---------------------------------------------------------------- the product
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 8;
+constexpr int kCus = 256;
+constexpr uint32_t kOutside = 0x7FFFFFF0u;      // an offset past every buffer: loads give 0
+
+// The codes of byte kByte times the scale, as a bf16 pair (exact).
+template <int kByte>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t codes, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, kByte));
 }
 
-__global__ __launch_bounds__(kThreads) void project_fp4_kernel(
+// Blocks whose scales a workgroup holds in LDS at a time, and the pitch of a
+// column's (an odd number of dwords, for the banks).
+constexpr int kSegBlocks = 256;
+inline __host__ __device__ int scale_pitch(int blocks) {
+  const int n = blocks < kSegBlocks ? blocks : kSegBlocks;
+  return ((n + 3) / 4 | 1) * 4;
+}
+
+// Dwords of scales a thread brings in.
+template <int kN>
+constexpr int scale_batch() {
+  return (16 * kN * (kSegBlocks / 4 + 1) + kWaves * 64 - 1) / (kWaves * 64);
+}
+
+// LDS: the scales, then each wave's two halves of a step of x; afterwards the
+// partial sums [2][waves][16][kPitch].
+template <int kM>
+constexpr int x_half_bytes() { return 16 * kM * 128; }
+template <int kM, int kN>
+size_t project_lds() {
+  const size_t loop = scale_batch<kN>() * kWaves * 64 * sizeof(uint32_t) + kWaves * 2 * x_half_bytes<kM>();
+  return std::max(loop, sizeof(float) * std::min(kM, 2) * kWaves * 16 * (16 * kN + 4));
+}
+
+// Columns 16 * kN and tokens 16 * kM of a workgroup; its waves take the steps
+// of 4 blocks in turn.
+template <int kM, int kN>
+__global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
     const uint16_t *__restrict__ x, const uint8_t *__restrict__ codes,
-    const uint8_t *__restrict__ scales, uint16_t *__restrict__ out, int T, int K, int N) {
-  const int lane = threadIdx.x & 63;
-  const int64_t n = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-  if (n >= N) return;
-  const int blocks = K / 32;
-  for (int t = 0; t < T; ++t) {
-    float sum = 0.0f;
-    for (int b = lane; b < blocks; b += 64) {
-      const u32x4 q = *reinterpret_cast<const u32x4 *>(codes + (n * blocks + b) * 16);
-      const uint16_t *xt = x + int64_t(t) * K + 32 * b;
-      float part = 0.0f;
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t c = (q[i / 8] >> (4 * (i % 8))) & 15u;
-        part = fmaf(__uint_as_float(uint32_t(xt[i]) << 16), e2m1_to_float(c), part);
-      }
-      sum += ldexpf(part, int(scales[n * blocks + b]) - 127);
+    const uint8_t *__restrict__ scales, uint16_t *__restrict__ out, int T, int K, int N,
+    int tiles_m) {
+  constexpr int kTm = 16 * kM, kTn = 16 * kN, kPitch = kTn + 4;
+  constexpr int kHalf = x_half_bytes<kM>();
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Token tiles of one column tile are 8 workgroups apart: on one XCD, at one time.
+  const int tm = int(blockIdx.x / 8) % tiles_m, tn = int(blockIdx.x / 8) / tiles_m * 8 + int(blockIdx.x % 8);
+  const int64_t n0 = int64_t(tn) * kTn;
+  if (n0 >= N) return;                           // the whole workgroup
+  const int64_t m0 = int64_t(tm) * kTm;
+  const int blocks = K / 32, steps = (blocks + 3) / 4;
+  const __amdgpu_buffer_rsrc_t rx = gemm::make_rsrc(x + m0 * K, (T - m0) * K * 2);
+  const __amdgpu_buffer_rsrc_t rc = gemm::make_rsrc(codes + n0 * (K / 2), (N - n0) * (K / 2));
+  const __amdgpu_buffer_rsrc_t rs = gemm::make_rsrc(scales + n0 * blocks, (N - n0) * blocks);
+
+  // The scales of a segment to LDS: the first one's requested in one batch ahead
+  // of all else, later ones' (K above 8192) in a loop.
+  const int pitch = scale_pitch(blocks), words = pitch / 4;
+  const bool by_word = blocks % 4 == 0 && reinterpret_cast<uintptr_t>(scales) % 4 == 0;
+  uint32_t *const sc_lds = reinterpret_cast<uint32_t *>(smem);
+  auto scale_offset = [&](int i, int b0) {
+    const int row = i / words, at = b0 + 4 * (i - row * words);
+    return row < kTn && at < blocks ? uint32_t(row) * blocks + at : kOutside;
+  };
+  auto load_scale = [&](uint32_t off) {
+    if (by_word) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+    uint32_t v = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(rs, off + e, 0, 0)) << (8 * e);
+    return v;
+  };
+  constexpr int kBatch = scale_batch<kN>();
+  uint32_t sreg[kBatch];
+  if (by_word) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      sreg[k] = __builtin_amdgcn_raw_buffer_load_b32(rs, scale_offset(tid + k * kWaves * 64, 0), 0, 0);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) sreg[k] = load_scale(scale_offset(tid + k * kWaves * 64, 0));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  // Weights: lane (r, g) takes block g of the step for column r of each 16.
+  constexpr int kSlots = 2;
+  u32x4 fc[kSlots][kN];
+  const uint32_t c_row = uint32_t(r) * (K / 2) + 16 * g;
+  auto load_w = [&](const int slot, int step) {
+    const bool in = 4 * step + g < blocks;
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      fc[slot][j] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     rc, in ? c_row + uint32_t(16 * j) * (K / 2) + 64 * step : kOutside, 0, 0));
+  };
+
+  // x: half a step (64 k, 128 bytes of each token) at a time into the wave's own
+  // LDS, 8 tokens an instruction.  16-byte piece p of token t lies at p ^ (t / 2 % 8),
+  // so that the 16 tokens of a fragment read different banks.
+  uint8_t *const xs = smem + kBatch * kWaves * 64 * 4 + wave * 2 * kHalf;
+  uint32_t x_off[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    x_off[u] = uint32_t(8 * u + lane / 8) * K * 2 + 16 * ((lane % 8) ^ (4 * u + lane / 16));
+  auto load_x = [&](const int h, int step) {
+    const bool in = step < steps;
+#pragma unroll
+    for (int u = 0; u < 2 * kM; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, xs + h * kHalf + u * 1024, 16,
+          in ? x_off[u % 2] + uint32_t(u / 2 * 16) * K * 2 + 256 * step + 128 * h : kOutside, 0, 0, 0);
+  };
+
+  f32x4v acc[kN][kM];
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+#pragma unroll
+    for (int t = 0; t < kM; ++t) acc[j][t] = f32x4v{};
+  auto multiply = [&](const int slot, int step) {
+    // Lane group g holds block g; it needs dword g of each.
+    uint32_t w[kN][4], sc[kN];
+    const int at = step < steps ? 4 * (step % (kSegBlocks / 4)) : 0;      // any, past the last step
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const u32x4 c = fc[slot][j];
+      const auto c02 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+      const auto c13 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+      const auto c01 = __builtin_amdgcn_permlane16_swap(c02[0], c13[0], false, false);
+      const auto c23 = __builtin_amdgcn_permlane16_swap(c02[1], c13[1], false, false);
+      w[j][0] = c01[0], w[j][1] = c01[1], w[j][2] = c23[0], w[j][3] = c23[1];
+      sc[j] = *reinterpret_cast<const uint32_t *>(smem + (16 * j + r) * pitch + at);
     }
-    for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-    if (lane == 0) out[int64_t(t) * N + n] = f32_to_bf16(sum);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // This half landed: what was requested after it is the other half and
+      // one step's weights.
+      __builtin_amdgcn_s_waitcnt(gemm::waitcnt(2 * kM + kN, 15));
+      asm volatile("" ::: "memory");
+      u32x4 fx[2][kM];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < kM; ++t)
+          fx[i][t] = *reinterpret_cast<const u32x4 *>(
+              xs + h * kHalf + (16 * t + r) * 128 + 16 * ((4 * i + g) ^ (r / 2)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = 2 * h + i;
+        if (4 * step + b < blocks) {               // uniform: past K there is no x
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            const uint32_t f = (sc[j] >> (8 * b) & 0xFFu) << 23;
+            const float scale = __uint_as_float(max(f, 0x00400000u));    // byte 0: 2^-127
+            const u32x4 v = {e2m1_pair<0>(w[j][b], scale), e2m1_pair<1>(w[j][b], scale),
+                             e2m1_pair<2>(w[j][b], scale), e2m1_pair<3>(w[j][b], scale)};
+#pragma unroll
+            for (int t = 0; t < kM; ++t)
+              acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, fx[i][t]), acc[j][t], 0, 0, 0);
+          }
+        }
+      }
+      // The half is in registers: the next step's may overwrite it.
+      __builtin_amdgcn_s_waitcnt(gemm::waitcnt(63, 0));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      load_x(h, step + kWaves);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  load_w(0, wave);
+  __builtin_amdgcn_sched_barrier(0);
+  load_x(0, wave);
+  load_x(1, wave);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(1, wave + kWaves);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) sc_lds[tid + k * kWaves * 64] = sreg[k];
+  // A segment's steps are a multiple of kSlots * kWaves (but the last one's).
+  for (int seg = 0; seg < steps; seg += kSegBlocks / 4) {
+    if (seg > 0) {
+      __syncthreads();
+      for (int i = tid; i < kTn * words; i += kWaves * 64)
+        sc_lds[i] = load_scale(scale_offset(i, 4 * seg));
+    }
+    __syncthreads();
+    const int end = min(steps, seg + kSegBlocks / 4);
+    for (int s = seg + wave; s < end; s += kSlots * kWaves) {
+#pragma unroll
+      for (int p = 0; p < kSlots; ++p) {
+        multiply(p, s + kWaves * p);
+        load_w(p, s + kWaves * (p + kSlots));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // The waves' sums added in wave order, 16 tokens at a time.  D of a 16 x 16
+  // block: lane l holds token l % 16, columns 4 (l / 16) .. + 3.
+  using Part = float[kWaves][16][kPitch];
+  Part *red = reinterpret_cast<Part *>(smem);
+  __builtin_amdgcn_s_waitcnt(gemm::waitcnt(0, 0));       // the last, unread x
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < kM; ++t) {
+    Part &part = red[t % 2];
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      *reinterpret_cast<f32x4v *>(&part[wave][r][16 * j + 4 * g]) = acc[j][t];
+    __syncthreads();
+    for (int i = tid; i < 16 * kTn; i += kWaves * 64) {
+      const int m = i / kTn, n = i % kTn;
+      float sum = part[0][m][n];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += part[w][m][n];
+      const int64_t row = m0 + 16 * t + m;
+      if (row < T && n0 + n < N) out[row * N + n0 + n] = f32_to_bf16(sum);
+    }
+  }
+}
+
+template <int kM, int kN>
+hipError_t launch_tile(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                       uint16_t *out, int32_t T, int32_t K, int32_t N, hipStream_t stream) {
+  const int64_t tiles_m = (T + 16 * kM - 1) / (16 * kM);
+  const int64_t tiles_n = (int64_t(N) + 16 * kN - 1) / (16 * kN);
+  const size_t lds = project_lds<kM, kN>();
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&project_fp4_kernel<kM, kN>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((project_fp4_kernel<kM, kN>), dim3(unsigned((tiles_n + 7) / 8 * 8 * tiles_m)),
+                     dim3(kWaves * 64), lds, stream, x, codes, scales, out, T, K, N, int(tiles_m));
+  return hipGetLastError();
+}
+
+template <int kM>
+hipError_t by_columns(int n, const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                      uint16_t *out, int32_t T, int32_t K, int32_t N, hipStream_t stream) {
+  switch (n) {
+    case 1: return launch_tile<kM, 1>(x, codes, scales, out, T, K, N, stream);
+    case 2: return launch_tile<kM, 2>(x, codes, scales, out, T, K, N, stream);
+    case 3: return launch_tile<kM, 3>(x, codes, scales, out, T, K, N, stream);
+    case 4: return launch_tile<kM, 4>(x, codes, scales, out, T, K, N, stream);
+    default: return launch_tile<kM, 5>(x, codes, scales, out, T, K, N, stream);
   }
 }
 
@@ -97,13 +334,25 @@ hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t 
   return hipGetLastError();
 }
 
+// The tile with the least to pull through a CU's vector cache: per 32 k a tile
+// takes 64 bytes a token and 17 a column, and the CUs take ceil(tiles / 256)
+// tiles each.
 hipError_t launch_project_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
                               uint16_t *out, int32_t T, int32_t K, int32_t N,
                               hipStream_t stream) {
-  const int per = kThreads / 64;
-  hipLaunchKernelGGL(project_fp4_kernel, dim3(unsigned((int64_t(N) + per - 1) / per)),
-                     dim3(kThreads), 0, stream, x, codes, scales, out, T, K, N);
-  return hipGetLastError();
+  int best_m = 1, best_n = 1;
+  int64_t best = INT64_MAX;
+  for (const int m : {1, 2, 4})
+    for (int n = 1; n <= 5; ++n) {
+      const int64_t tiles = ((int64_t(T) + 16 * m - 1) / (16 * m)) * ((int64_t(N) + 16 * n - 1) / (16 * n));
+      const int64_t cost = (tiles + kCus - 1) / kCus * (64 * 16 * std::min<int64_t>(m, (T + 15) / 16) + 17 * 16 * n);
+      if (cost < best) best = cost, best_m = m, best_n = n;
+    }
+  switch (best_m) {
+    case 1: return by_columns<1>(best_n, x, codes, scales, out, T, K, N, stream);
+    case 2: return by_columns<2>(best_n, x, codes, scales, out, T, K, N, stream);
+    default: return by_columns<4>(best_n, x, codes, scales, out, T, K, N, stream);
+  }
 }
 
 }  // namespace engram
