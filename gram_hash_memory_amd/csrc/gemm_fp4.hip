@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
   auto multiply = [&](const int slot, int step) {
     // Lane group g holds block g; it needs dword g of each.
     uint32_t w[kN][4], sc[kN];
-    const int at = step < steps ? 4 * (step % (kSegBlocks / 4)) : 0;      // any, past the last step
+    const int at = 4 * (step % (kSegBlocks / 4));
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const u32x4 c = fc[slot][j];
@@ -267,6 +267,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
     for (int s = seg + wave; s < end; s += kSlots * kWaves) {
 #pragma unroll
       for (int p = 0; p < kSlots; ++p) {
+        if (p > 0 && s + kWaves * p >= end) break;
         multiply(p, s + kWaves * p);
         load_w(p, s + kWaves * (p + kSlots));
         __builtin_amdgcn_sched_barrier(0);
