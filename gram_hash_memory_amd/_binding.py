@@ -165,9 +165,17 @@ def _check(status: int) -> None:
         raise EngramError(status, engram_last_error())
 
 
+# The current stream's handle without building a torch.cuda.Stream around it: 0.2 us
+# instead of 2.8 us, of some 10 us that a small call took on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or _raw_device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -175,6 +183,9 @@ def _dptr(t, dtype, min_numel: int = 0, name: str = "tensor"):
     """Device pointer of a contiguous GPU tensor with at least min_numel elements."""
     if t is None:
         return None
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and t.numel() >= min_numel):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:

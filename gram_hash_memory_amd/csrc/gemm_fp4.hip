@@ -305,9 +305,11 @@ hipError_t launch_tile(const uint16_t *x, const uint8_t *codes, const uint8_t *s
   const int64_t tiles_m = (T + 16 * kM - 1) / (16 * kM);
   const int64_t tiles_n = (int64_t(N) + 16 * kN - 1) / (16 * kN);
   const size_t lds = project_lds<kM, kN>();
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&project_fp4_kernel<kM, kN>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-  if (e != hipSuccess) return e;
+  if (lds > 65536) {                             // what a launch may have without asking
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&project_fp4_kernel<kM, kN>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((project_fp4_kernel<kM, kN>), dim3(unsigned((tiles_n + 7) / 8 * 8 * tiles_m)),
                      dim3(kWaves * 64), lds, stream, x, codes, scales, out, T, K, N, int(tiles_m));
   return hipGetLastError();
