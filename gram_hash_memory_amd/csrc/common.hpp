@@ -176,8 +176,9 @@ struct QkRope {
   int32_t T, q_heads, kv_heads, head_dim, rotary_dim;
   float eps;
   // From qk_rope_plan: the heads a token has here (the values' ones with a
-  // cache), and how many of them a wave takes.
-  int32_t heads, heads_per_wave, waves_per_token;
+  // cache), and how the waves share them.
+  float inv_dim;
+  int32_t heads, passes_per_wave, waves_per_token;
 };
 int64_t qk_rope_plan(QkRope *a);            // workgroups
 hipError_t launch_qk_norm_rope(const QkRope &a, bool interleaved, int64_t blocks,

@@ -1,9 +1,9 @@
 // The paged key-value cache: addressing, and the 8-bit format's rounding.
 //
 // A head's head_dim values of one token are contiguous in the cache.  The
-// kernels that move them give each such row to LP lanes (head_dim / 16
-// rounded up to a power of two; lanes past head_dim / 16 idle), 16
-// consecutive values a lane: a 32-value block of the 8-bit format is then two
+// kernels that move them give a lane 8 consecutive values at a time, 16 bytes
+// of bf16, neighbouring lanes neighbouring ones: every load and store of a
+// wave is then of whole runs, and a 32-value block of the 8-bit format is four
 // neighbouring lanes.
 #pragma once
 
@@ -15,11 +15,6 @@ namespace kvc {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
-inline int lanes_per_row(int head_dim) {
-  const int n = head_dim / 16;
-  return n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;
-}
-
 // The index of a place's row among all rows of the cache.
 __device__ __forceinline__ int64_t row_index(const CacheView &c, int64_t slot, int head) {
   const int64_t page = slot >> c.page_shift;
@@ -27,56 +22,70 @@ __device__ __forceinline__ int64_t row_index(const CacheView &c, int64_t slot, i
   return ((page * c.kv_heads + head) << c.page_shift) + in_page;
 }
 
+// 16 bytes (or 8) past the caches where there is much to move once: a copy's
+// stores otherwise push out what is still to be read, and written lines wait in
+// the caches for their turn (32768 tokens read back: 55.3 us with plain
+// accesses, 50.7 us so; norm and rotation of 8192 tokens 37.8 and 31.3 us).
+template <bool kOnce, typename V = u32x4>
+__device__ __forceinline__ V load16(const void *p) {
+  if constexpr (kOnce) return __builtin_nontemporal_load(static_cast<const V *>(p));
+  else return *static_cast<const V *>(p);
+}
+template <bool kOnce>
+__device__ __forceinline__ void save16(void *p, u32x4 v) {
+  if constexpr (kOnce) __builtin_nontemporal_store(v, static_cast<u32x4 *>(p));
+  else *static_cast<u32x4 *>(p) = v;
+}
+
 __device__ __forceinline__ bool slot_ok(const CacheView &c, int64_t slot) {
   return slot >= 0 && slot < c.slots;
 }
 
-// 16 bf16 values (8 dwords, value 2i in the low half of dword i) of a lane to
-// e4m3 codes with the scale that they share with the neighbouring lane's.
-// The scale is 2^e with e the smallest that brings the block's largest finite
-// magnitude m 2^E (1 <= m < 2) to 448 = 1.75 * 2^8 or below: E - 8, one more
-// where m > 1.75; at least -95, so that 2^-e is a normal fp32 number, and the
-// products with it are exact.  All lanes of the wave run this.
-__device__ __forceinline__ uint32_t quantize16(const uint32_t (&w)[8], uint32_t (&codes)[4]) {
+// 8 bf16 values of a lane to e4m3 codes with the scale that the four lanes of
+// its block share.  The scale is 2^e with e the smallest that brings the
+// block's largest finite magnitude m 2^E (1 <= m < 2) to 448 = 1.75 * 2^8 or
+// below: E - 8, one more where m > 1.75; at least -95, so that 2^-e is a normal
+// fp32 number, and the products with it are exact.  All lanes of the wave run
+// this.
+__device__ __forceinline__ uint32_t quantize8(const u32x4 w, u32x2 *codes) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
     top = max(top, lo < 0x7F80u ? lo : 0u);
     top = max(top, hi < 0x7F80u ? hi : 0u);
   }
   top = max(top, uint32_t(__shfl_xor(int(top), 1)));
+  top = max(top, uint32_t(__shfl_xor(int(top), 2)));
   int e = int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u);
   e = top == 0 ? 0 : max(e, -95);
   const float inv = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     int p = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(w[2 * i]) * inv, bf16_hi(w[2 * i]) * inv, 0,
                                             false);
     p = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(w[2 * i + 1]) * inv,
                                         bf16_hi(w[2 * i + 1]) * inv, p, true);
-    codes[i] = uint32_t(p);
+    (*codes)[i] = uint32_t(p);
   }
   return uint32_t(e + 127);
 }
 
-// A lane's 16 values into the cache's row `row` (ok: this lane has a place to
-// write to).  All lanes of the wave run this.
+// Values 8 piece .. 8 piece + 7 of the cache's row `row` (ok: this lane has a
+// place to write to); a block's four lanes are 4-aligned neighbours.  All lanes
+// of the wave run this.
 template <bool kMx>
-__device__ __forceinline__ void store16(void *data, uint8_t *scales, int head_dim, int64_t row,
-                                        int sub, bool ok, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void store8(void *data, uint8_t *scales, int head_dim, int64_t row,
+                                       int piece, bool ok, const u32x4 w) {
   if constexpr (kMx) {
-    uint32_t codes[4];
-    const uint32_t byte = quantize16(w, codes);
+    u32x2 codes;
+    const uint32_t byte = quantize8(w, &codes);
     if (!ok) return;
-    uint8_t *dst = static_cast<uint8_t *>(data) + row * head_dim + 16 * sub;
-    *reinterpret_cast<u32x4 *>(dst) = u32x4{codes[0], codes[1], codes[2], codes[3]};
-    if (sub % 2 == 0) scales[row * (head_dim / 32) + sub / 2] = uint8_t(byte);
+    *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(data) + row * head_dim + 8 * piece) = codes;
+    if (piece % 4 == 0) scales[row * (head_dim / 32) + piece / 4] = uint8_t(byte);
   } else {
     if (!ok) return;
-    u32x4 *dst = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(data) + row * head_dim + 16 * sub);
-    dst[0] = u32x4{w[0], w[1], w[2], w[3]};
-    dst[1] = u32x4{w[4], w[5], w[6], w[7]};
+    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(data) + row * head_dim + 8 * piece) = w;
   }
 }
 

@@ -4,7 +4,7 @@
 //   y = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos - b sin, b cos + a sin)
 //
 // Bound by the bytes of qkv, q and k.  A wave takes a token's heads, LP lanes
-// a head (kv_cache.hpp), so a token's angles are formed once a wave, one a
+// a head, so a token's angles are formed once a wave, one a
 // lane: position * inv_freq in fp64, in turns, less the nearest whole number
 // (an angle at position 10^6 in fp32 would be off by 0.06), then sine and
 // cosine of the remaining half turn in fp32.  A lane holds two pieces of 8
@@ -20,6 +20,8 @@ namespace {
 using namespace kvc;
 
 constexpr int kMaxPairs = ENGRAM_MAX_ATTN_HEAD_DIM / 2;
+constexpr int kMaxPasses = 3;             // of a wave
+constexpr int64_t kFewWaves = 4096;
 constexpr int kRowShorts = 1024;          // 64 / LP rows of 16 LP values
 
 __device__ __forceinline__ void wave_sync() {
@@ -35,9 +37,16 @@ __device__ __forceinline__ void unpack8(const u32x4 q, float *x) {
   for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(q[i]), x[2 * i + 1] = bf16_hi(q[i]);
 }
 
+// Lanes of a head, 16 values each: head_dim / 16 rounded up to a power of two,
+// at least 4 (a block of the cache's 8-bit format); those past head_dim / 16 idle.
+inline int lanes_per_row(int head_dim) {
+  const int n = head_dim / 16;
+  return n <= 4 ? 4 : n <= 8 ? 8 : 16;
+}
+
 enum CacheMode { kNoCache, kBf16, kMxfp8 };
 
-template <int LP, bool kInter, CacheMode kMode>
+template <int LP, bool kInter, CacheMode kMode, int kPass>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkRope a) {
   constexpr int kRows = 64 / LP;
   __shared__ __attribute__((aligned(16))) float2 cs_lds[kWaves][kMaxPairs];
@@ -48,9 +57,43 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkRope a) {
   const int64_t id = int64_t(blockIdx.x) * kWaves + wave;
   const int64_t t = id / a.waves_per_token;
   if (t >= a.T) return;                              // the whole wave; no barrier below
-  const int first = int(id - t * a.waves_per_token) * a.heads_per_wave;
-  const int last = min(a.heads, first + a.heads_per_wave);
+  const int part = int(id - t * a.waves_per_token);
+  const int passes = (a.heads + kRows - 1) / kRows;
+  const int pass0 = passes * part / a.waves_per_token, pass1 = passes * (part + 1) / a.waves_per_token;
   const int D = a.head_dim, half = a.rotary_dim / 2;
+
+  // All of the wave's rows are requested before anything is waited for.
+  const bool lane_on = 16 * sub < D;
+  const int nrot = a.rotary_dim / 16;
+  const bool rotated = sub < nrot;
+  const int pa = 8 * (rotated && !kInter ? sub : 2 * sub);
+  const int pb = rotated && !kInter ? pa + 8 * nrot : pa + 8;
+  const uint16_t *row = a.qkv + t * a.token_stride;
+  u32x4 ra[kPass], rb[kPass], wq[2], wk[2];
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    const int h = (pass0 + i) * kRows + in_wave;
+    const bool is_v = h >= a.q_heads + a.kv_heads;
+    ra[i] = rb[i] = u32x4{};
+    if (pass0 + i < pass1 && h < a.heads && lane_on) {
+      ra[i] = load16<kPass != 1>(row + h * D + (is_v ? 16 * sub : pa));
+      rb[i] = load16<kPass != 1>(row + h * D + (is_v ? 16 * sub + 8 : pb));
+    }
+  }
+  wq[0] = wq[1] = wk[0] = wk[1] = u32x4{};
+  if (lane_on) {
+    wq[0] = *reinterpret_cast<const u32x4 *>(a.q_weight + pa);
+    wq[1] = *reinterpret_cast<const u32x4 *>(a.q_weight + pb);
+    wk[0] = *reinterpret_cast<const u32x4 *>(a.k_weight + pa);
+    wk[1] = *reinterpret_cast<const u32x4 *>(a.k_weight + pb);
+  }
+  int64_t slot = -1;
+  bool slot_in = false;
+  if constexpr (kMode != kNoCache) {
+    slot = a.slots[t];
+    slot_in = slot_ok(a.cache, slot);
+    if (!slot_in && slot != -1 && a.bad_slots && part == 0 && lane == 0) atomicAdd(a.bad_slots, 1);
+  }
 
   // The wave's angles, and this lane's 8 of them.
   float2 *cs = cs_lds[wave];
@@ -62,11 +105,6 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkRope a) {
     cs[i] = float2{c, s};
   }
   wave_sync();
-  const bool lane_on = 16 * sub < D;
-  const int nrot = a.rotary_dim / 16;
-  const bool rotated = sub < nrot;
-  const int pa = 8 * (rotated && !kInter ? sub : 2 * sub);
-  const int pb = rotated && !kInter ? pa + 8 * nrot : pa + 8;
   float cosv[8], sinv[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -74,43 +112,28 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkRope a) {
     cosv[j] = v.x, sinv[j] = v.y;
   }
 
-  const uint16_t *row = a.qkv + t * a.token_stride;
-  int64_t slot = -1;
-  bool slot_in = false;
-  if constexpr (kMode != kNoCache) {
-    slot = a.slots[t];
-    slot_in = slot_ok(a.cache, slot);
-    if (!slot_in && slot != -1 && a.bad_slots && first == 0 && lane == 0) atomicAdd(a.bad_slots, 1);
-  }
-
-  for (int h0 = first; h0 < last; h0 += kRows) {
-    const int h = h0 + in_wave;
-    const bool on = h < last && lane_on;
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    if (pass0 + i >= pass1) break;
+    const int h = (pass0 + i) * kRows + in_wave;
+    const bool on = h < a.heads && lane_on;
     const bool is_v = h >= a.q_heads + a.kv_heads;
     const bool is_k = !is_v && h >= a.q_heads;
     const int oa = is_v ? 16 * sub : pa, ob = is_v ? 16 * sub + 8 : pb;
-    u32x4 ra{}, rb{};
-    if (on) {
-      ra = *reinterpret_cast<const u32x4 *>(row + h * D + oa);
-      rb = *reinterpret_cast<const u32x4 *>(row + h * D + ob);
-    }
     float x[16];
-    unpack8(ra, x);
-    unpack8(rb, x + 8);
+    unpack8(ra[i], x);
+    unpack8(rb[i], x + 8);
     float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
     for (int m = 1; m < LP; m *= 2) ss += __shfl_xor(ss, m);
-    const float r = 1.0f / sqrtf(ss / float(D) + a.eps);
-    float w[16] = {};
-    if (on) {
-      const uint16_t *wt = is_k ? a.k_weight : a.q_weight;
-      unpack8(*reinterpret_cast<const u32x4 *>(wt + pa), w);
-      unpack8(*reinterpret_cast<const u32x4 *>(wt + pb), w + 8);
-    }
+    const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+    float w[16];
+    unpack8(is_k ? wk[0] : wq[0], w);
+    unpack8(is_k ? wk[1] : wq[1], w + 8);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+    for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
     if (rotated) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -122,47 +145,53 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkRope a) {
     }
     if (!is_v) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ra[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        rb[i] = pack_bf16x2(x[8 + 2 * i], x[9 + 2 * i]);
+      for (int e = 0; e < 4; ++e) {
+        ra[i][e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        rb[i][e] = pack_bf16x2(x[8 + 2 * e], x[9 + 2 * e]);
       }
     }
     if (on && !is_v) {
       uint16_t *dst = !is_k ? a.q + (t * a.q_heads + h) * D
                             : a.k ? a.k + (t * a.kv_heads + h - a.q_heads) * D : nullptr;
       if (dst) {
-        *reinterpret_cast<u32x4 *>(dst + oa) = ra;
-        *reinterpret_cast<u32x4 *>(dst + ob) = rb;
+        save16<kPass != 1>(dst + oa, ra[i]);
+        save16<kPass != 1>(dst + ob, rb[i]);
       }
     }
     if constexpr (kMode != kNoCache) {
-      if (h0 + kRows <= a.q_heads) continue;         // only queries in this pass
-      // Keys and values to 16 consecutive values a lane, by way of LDS.
+      if ((pass0 + i + 1) * kRows <= a.q_heads) continue;      // only queries in this pass
+      // Keys and values to 8 consecutive ones a lane and step, by way of LDS.
       uint16_t *mine = row_lds[wave] + in_wave * 16 * LP;
       if (lane_on) {
-        *reinterpret_cast<u32x4 *>(mine + oa) = ra;
-        *reinterpret_cast<u32x4 *>(mine + ob) = rb;
+        *reinterpret_cast<u32x4 *>(mine + oa) = ra[i];
+        *reinterpret_cast<u32x4 *>(mine + ob) = rb[i];
       }
       wave_sync();
-      const u32x4 lo = *reinterpret_cast<const u32x4 *>(mine + 16 * sub);
-      const u32x4 hi = *reinterpret_cast<const u32x4 *>(mine + 16 * sub + 8);
+      const u32x4 o[2] = {*reinterpret_cast<const u32x4 *>(mine + 8 * sub),
+                          *reinterpret_cast<const u32x4 *>(mine + 8 * (LP + sub))};
       wave_sync();
-      uint32_t o[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = lo[i], o[4 + i] = hi[i];
-      const bool put = on && slot_in && (is_k || is_v);
+      const bool put = h < a.heads && slot_in && (is_k || is_v);
       const int head = is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
-      store16<kMode == kMxfp8>(is_v ? a.cache.v : a.cache.k,
-                               is_v ? a.cache.v_scales : a.cache.k_scales, D,
-                               put ? row_index(a.cache, slot, head) : 0, sub, put, o);
+      const int64_t to = put ? row_index(a.cache, slot, head) : 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int piece = e * LP + sub;
+        store8<kMode == kMxfp8>(is_v ? a.cache.v : a.cache.k,
+                                is_v ? a.cache.v_scales : a.cache.k_scales, D, to, piece,
+                                put && 8 * piece < D, o[e]);
+      }
     }
   }
 }
 
 template <int LP, bool kInter, CacheMode kMode>
 void launch(const QkRope &a, unsigned blocks, hipStream_t stream) {
-  hipLaunchKernelGGL((qk_norm_rope_kernel<LP, kInter, kMode>), dim3(blocks), dim3(kThreads), 0,
-                     stream, a);
+  if (a.passes_per_wave == 1)
+    hipLaunchKernelGGL((qk_norm_rope_kernel<LP, kInter, kMode, 1>), dim3(blocks), dim3(kThreads), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((qk_norm_rope_kernel<LP, kInter, kMode, kMaxPasses>), dim3(blocks),
+                       dim3(kThreads), 0, stream, a);
 }
 
 template <int LP, bool kInter>
@@ -180,10 +209,14 @@ void by_pairs(const QkRope &a, bool inter, unsigned blocks, hipStream_t stream) 
 
 }  // namespace
 
+// A wave forms its token's angles, so it takes several passes of 64 / LP heads
+// where there are waves enough.
 int64_t qk_rope_plan(QkRope *a) {
   a->heads = a->q_heads + (a->cache.k ? 2 : 1) * a->kv_heads;
-  a->heads_per_wave = a->heads;
-  a->waves_per_token = (a->heads + a->heads_per_wave - 1) / a->heads_per_wave;
+  a->inv_dim = 1.0f / float(a->head_dim);
+  const int rows = 64 / lanes_per_row(a->head_dim), passes = (a->heads + rows - 1) / rows;
+  a->passes_per_wave = int64_t(a->T) * passes <= kFewWaves ? 1 : kMaxPasses;
+  a->waves_per_token = (passes + a->passes_per_wave - 1) / a->passes_per_wave;
   return (int64_t(a->T) * a->waves_per_token + kWaves - 1) / kWaves;
 }
 
@@ -191,7 +224,6 @@ hipError_t launch_qk_norm_rope(const QkRope &a, bool interleaved, int64_t blocks
                                hipStream_t stream) {
   const unsigned n = unsigned(blocks);
   switch (lanes_per_row(a.head_dim)) {
-    case 2: by_pairs<2>(a, interleaved, n, stream); break;
     case 4: by_pairs<4>(a, interleaved, n, stream); break;
     case 8: by_pairs<8>(a, interleaved, n, stream); break;
     default: by_pairs<16>(a, interleaved, n, stream);
