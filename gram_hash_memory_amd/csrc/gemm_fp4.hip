@@ -96,13 +96,13 @@ constexpr int scale_batch() {
   return (16 * kN * (kSegBlocks / 4 + 1) + kWaves * 64 - 1) / (kWaves * 64);
 }
 
-// LDS: the scales, then each wave's two halves of a step of x; afterwards the
+// LDS: the scales, each wave's 1 KB for its weights' order, each wave's two halves of a step of x; afterwards the
 // partial sums [2][waves][16][kPitch].
 template <int kM>
 constexpr int x_half_bytes() { return 16 * kM * 128; }
 template <int kM, int kN>
 size_t project_lds() {
-  const size_t loop = scale_batch<kN>() * kWaves * 64 * sizeof(uint32_t) + kWaves * 2 * x_half_bytes<kM>();
+  const size_t loop = scale_batch<kN>() * kWaves * 64 * sizeof(uint32_t) + kWaves * (1024 + 2 * x_half_bytes<kM>());
   return std::max(loop, sizeof(float) * std::min(kM, 2) * kWaves * 16 * (16 * kN + 4));
 }
 
@@ -158,12 +158,17 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  // Weights: lane (r, g) takes block g of the step for column r of each 16.
+  // Weights: 4 neighbouring lanes request a step's 4 blocks of a column, 64 bytes
+  // (the vector cache takes a clock per run of addresses in 16 lanes: 16 columns
+  // in 16 lanes cost 4 times as many).
   constexpr int kSlots = 2;
   u32x4 fc[kSlots][kN];
-  const uint32_t c_row = uint32_t(r) * (K / 2) + 16 * g;
+  const uint32_t c_row = uint32_t(lane / 4) * (K / 2) + 16 * (lane % 4);
+  uint8_t *const ws = smem + kBatch * kWaves * 64 * 4 + wave * 1024;
+  uint8_t *const w_put = ws + 64 * (lane / 4) + 16 * ((lane % 4) ^ (lane / 16));
+  const uint8_t *const w_get = ws + 64 * r + 4 * g;
   auto load_w = [&](const int slot, int step) {
-    const bool in = 4 * step + g < blocks;
+    const bool in = 4 * step + lane % 4 < blocks;
 #pragma unroll
     for (int j = 0; j < kN; ++j)
       fc[slot][j] = __builtin_bit_cast(
@@ -174,7 +179,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
   // x: half a step (64 k, 128 bytes of each token) at a time into the wave's own
   // LDS, 8 tokens an instruction.  16-byte piece p of token t lies at p ^ (t / 2 % 8),
   // so that the 16 tokens of a fragment read different banks.
-  uint8_t *const xs = smem + kBatch * kWaves * 64 * 4 + wave * 2 * kHalf;
+  uint8_t *const xs = smem + (kBatch * kWaves * 64 * 4 + kWaves * 1024) + wave * 2 * kHalf;
   uint32_t x_off[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u)
@@ -194,17 +199,16 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
 #pragma unroll
     for (int t = 0; t < kM; ++t) acc[j][t] = f32x4v{};
   auto multiply = [&](const int slot, int step) {
-    // Lane group g holds block g; it needs dword g of each.
+    // From the order of the request to that of the matrix cores: lane group g's
+    // dword g of each of the 4 blocks, by way of 1 KB of the wave's own LDS (whose
+    // accesses keep their order).
     uint32_t w[kN][4], sc[kN];
     const int at = 4 * (step % (kSegBlocks / 4));
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const u32x4 c = fc[slot][j];
-      const auto c02 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
-      const auto c13 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
-      const auto c01 = __builtin_amdgcn_permlane16_swap(c02[0], c13[0], false, false);
-      const auto c23 = __builtin_amdgcn_permlane16_swap(c02[1], c13[1], false, false);
-      w[j][0] = c01[0], w[j][1] = c01[1], w[j][2] = c23[0], w[j][3] = c23[1];
+      *reinterpret_cast<u32x4 *>(w_put) = fc[slot][j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[j][i] = *reinterpret_cast<const uint32_t *>(w_get + 16 * (i ^ (r / 4)));
       sc[j] = *reinterpret_cast<const uint32_t *>(smem + (16 * j + r) * pitch + at);
     }
 #pragma unroll

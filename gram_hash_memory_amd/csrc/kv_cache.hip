@@ -97,11 +97,11 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(
     const int64_t at = row_index(c, slot[i], r[i].head) * c.head_dim + 8 * sub;
     const void *data = r[i].is_v ? c.v : c.k;
     if constexpr (kMx) {
-      const u32x2 q = load16<(kPer > 1), u32x2>(static_cast<const uint8_t *>(data) + at);
+      const u32x2 q = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(data) + at);
       w[i][0] = q[0], w[i][1] = q[1];
       scale[i] = (r[i].is_v ? c.v_scales : c.k_scales)[at / 32];
     } else {
-      w[i] = load16<(kPer > 1)>(static_cast<const uint16_t *>(data) + at);
+      w[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(data) + at);
     }
   }
 #pragma unroll

@@ -22,14 +22,14 @@ __device__ __forceinline__ int64_t row_index(const CacheView &c, int64_t slot, i
   return ((page * c.kv_heads + head) << c.page_shift) + in_page;
 }
 
-// 16 bytes (or 8) past the caches where there is much to move once: a copy's
-// stores otherwise push out what is still to be read, and written lines wait in
-// the caches for their turn (32768 tokens read back: 55.3 us with plain
-// accesses, 50.7 us so; norm and rotation of 8192 tokens 37.8 and 31.3 us).
-template <bool kOnce, typename V = u32x4>
-__device__ __forceinline__ V load16(const void *p) {
-  if constexpr (kOnce) return __builtin_nontemporal_load(static_cast<const V *>(p));
-  else return *static_cast<const V *>(p);
+// 16 bytes past the caches where there is much to move once: the stores
+// otherwise push out what is still to be read, and written lines wait in the
+// caches for their turn (32768 tokens read back: 55.3 us with plain stores,
+// 50.7 us so; norm and rotation of 8192 tokens 37.8 and, its loads too, 31.3 us).
+template <bool kOnce>
+__device__ __forceinline__ u32x4 load16(const void *p) {
+  if constexpr (kOnce) return __builtin_nontemporal_load(static_cast<const u32x4 *>(p));
+  else return *static_cast<const u32x4 *>(p);
 }
 template <bool kOnce>
 __device__ __forceinline__ void save16(void *p, u32x4 v) {
