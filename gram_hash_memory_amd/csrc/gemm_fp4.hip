@@ -198,6 +198,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
   for (int j = 0; j < kN; ++j)
 #pragma unroll
     for (int t = 0; t < kM; ++t) acc[j][t] = f32x4v{};
+  // (A scale's byte goes to the exponent field, all that the conversion reads: byte 0 is 2^-127.)
+  auto convert = [&](uint32_t codes, uint32_t scales4, const int b) {
+    const float f = __uint_as_float((scales4 >> (8 * b) & 0xFFu) << 23);
+    return u32x4{e2m1_pair<0>(codes, f), e2m1_pair<1>(codes, f), e2m1_pair<2>(codes, f),
+                 e2m1_pair<3>(codes, f)};
+  };
   auto multiply = [&](const int slot, int step) {
     // From the order of the request to that of the matrix cores: lane group g's
     // dword g of each of the 4 blocks, by way of 1 KB of the wave's own LDS (whose
@@ -230,10 +236,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
         if (4 * step + b < blocks) {               // uniform: past K there is no x
 #pragma unroll
           for (int j = 0; j < kN; ++j) {
-            const uint32_t f = (sc[j] >> (8 * b) & 0xFFu) << 23;
-            const float scale = __uint_as_float(max(f, 0x00400000u));    // byte 0: 2^-127
-            const u32x4 v = {e2m1_pair<0>(w[j][b], scale), e2m1_pair<1>(w[j][b], scale),
-                             e2m1_pair<2>(w[j][b], scale), e2m1_pair<3>(w[j][b], scale)};
+            const u32x4 v = convert(w[j][b], sc[j], b);
 #pragma unroll
             for (int t = 0; t < kM; ++t)
               acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -279,26 +282,38 @@ __global__ __launch_bounds__(kWaves * 64, 1) void project_fp4_kernel(
     }
   }
 
-  // The waves' sums added in wave order, 16 tokens at a time.  D of a 16 x 16
-  // block: lane l holds token l % 16, columns 4 (l / 16) .. + 3.
-  using Part = float[kWaves][16][kPitch];
+  // The waves' sums added in wave order, up to 32 tokens at a time.  D of a 16 x
+  // 16 block: lane l holds token l % 16, columns 4 (l / 16) .. + 3.
+  constexpr int kTiles = kM < 2 ? 1 : 2;
+  using Part = float[kTiles * 16][kPitch];
   Part *red = reinterpret_cast<Part *>(smem);
   __builtin_amdgcn_s_waitcnt(gemm::waitcnt(0, 0));       // the last, unread x
-  __syncthreads();
+  const bool whole = N % 4 == 0;                         // 4 columns a store
 #pragma unroll
-  for (int t = 0; t < kM; ++t) {
-    Part &part = red[t % 2];
-#pragma unroll
-    for (int j = 0; j < kN; ++j)
-      *reinterpret_cast<f32x4v *>(&part[wave][r][16 * j + 4 * g]) = acc[j][t];
+  for (int t0 = 0; t0 < kM; t0 += kTiles) {
     __syncthreads();
-    for (int i = tid; i < 16 * kTn; i += kWaves * 64) {
-      const int m = i / kTn, n = i % kTn;
-      float sum = part[0][m][n];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) sum += part[w][m][n];
-      const int64_t row = m0 + 16 * t + m;
-      if (row < T && n0 + n < N) out[row * N + n0 + n] = f32_to_bf16(sum);
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        *reinterpret_cast<f32x4v *>(&red[wave][16 * t + r][16 * j + 4 * g]) = acc[j][t0 + t];
+    __syncthreads();
+    for (int i = tid; i < kTiles * 16 * (kTn / 4); i += kWaves * 64) {
+      const int m = i / (kTn / 4), n = 4 * (i % (kTn / 4));
+      f32x4v sum = *reinterpret_cast<const f32x4v *>(&red[0][m][n]);
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4v *>(&red[w][m][n]);
+      const int64_t row = m0 + 16 * t0 + m;
+      if (row >= T) continue;
+      uint16_t *dst = out + row * N + n0 + n;
+      if (whole) {
+        if (n0 + n < N)
+          *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n0 + n + e < N) dst[e] = f32_to_bf16(sum[e]);
+      }
     }
   }
 }
