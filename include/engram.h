@@ -564,6 +564,8 @@ ENGRAM_API size_t engram_paged_attention_workspace_bytes(int32_t n_seqs, int32_t
  *   table_width + p / page_size] (DEVICE int32).  lens DEVICE int32 [n_seqs]:
  *   the sequence's length, its newest token included; a length below 0 counts
  *   as 0, one above max_len or table_width * page_size as the smaller of these.
+ *   max_len at most 2^30, and at most 2^31 - 2^24 units of 128 places over all
+ *   sequences, key-value heads and blocks of 32 query heads.
  *   The places seen are max(0, len - window) .. len - 1 (window 0: all).
  *   Entries of the table for other places are not used, and what the cache
  *   holds there may be anything, NaN included.  The places of a page outside

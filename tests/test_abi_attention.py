@@ -178,6 +178,13 @@ class TestValidation:
                      (1, 7, 31, 32, 33, 100, 500, 1000, 4096, 4097, 50000, 131072, 1 << 20, (1 << 31) - 1)]
             assert sizes == sorted(sizes), (n, hq, hkv)
 
+    def test_paged_attention_rejects_lengths_past_32_bits_of_places(self, lib):
+        c = cache()
+        call = lambda max_len, n=1: lib.engram_paged_attention(  # noqa: E731
+            ctypes.byref(c), FAKE, FAKE, 4, FAKE, n, 8, max_len, 1.0, 0, FAKE, None, FAKE, 1 << 40, None, None)
+        assert call((1 << 30) + 1) == UNSUPPORTED
+        assert call(1 << 30, n=1 << 20) == UNSUPPORTED
+
     def test_fp4_rejects(self, lib):
         call = caller(lib.engram_quantize_mxfp4, ("w", "N", "K", "codes", "scales", "stream"),
                       dict(w=FAKE, N=8, K=64, codes=FAKE, scales=FAKE, stream=None))

@@ -291,6 +291,68 @@ def test_qk_norm_rope_into_the_cache(eg, fmt, ps, T, hq, hkv, D, rot, inter):
     same_cache(arrays2, held2)
 
 
+@pytest.mark.parametrize("fmt,ps,hkv,D", [("bf16", 16, 8, 128), ("mxfp8", 16, 8, 128), ("mxfp8", 32, 3, 96),
+                                          ("mxfp8", 8, 5, 224), ("bf16", 64, 1, 32), ("mxfp8", 16, 7, 64)])
+def test_cache_moves_of_many_tokens(eg, fmt, ps, hkv, D):
+    """Enough tokens that a thread moves several pieces; slots that are not there among them."""
+    rng = np.random.default_rng(D + hkv)
+    T = 2048 * 256 // (2 * hkv * (D // 8)) + 77
+    pages = -(-T // ps) + 1
+    arrays, held, handle = make_cache(eg, rng, fmt, pages, hkv, ps, D)
+    room = pages * ps
+    slots = rng.permutation(room)[:T].astype(np.int64)
+    slots[[2, T // 2, T - 1]] = [-1, room, -5]
+    x = bits(rng.normal(size=(T, 2 * hkv, D)))
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    row = dev(x)
+    eg.engram_cache_write(handle, row[:, :hkv], row[:, hkv:], dev(slots), bad)
+    # What it should hold, the oracle's rounding applied to all tokens at once.
+    ok = (slots >= 0) & (slots < room)
+    at = slots[ok]
+    for w, part in ((0, x[:, :hkv]), (1, x[:, hkv:])):
+        if fmt == "bf16":
+            arrays[w][at // ps, :, at % ps] = part[ok]
+        else:
+            arrays[w][at // ps, :, at % ps], arrays[w + 2][at // ps, :, at % ps] = oa.quantize_cache(part[ok])
+    same_cache(arrays, held)
+    k, v = Guarded((T, hkv, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    eg.engram_cache_read(handle, dev(slots), k.t, v.t, bad)
+    for got, which in ((k, 0), (v, 1)):
+        want = oa.cache_rows(arrays[which], arrays[which + 2], np.clip(slots, 0, room - 1))
+        want[~ok] = 0
+        assert np.array_equal(got.host(), bits(want))
+    assert bad.item() == 4
+
+
+@pytest.mark.parametrize("fmt,T,hq,hkv,D,rot,inter", [
+    ("mxfp8", 1500, 32, 8, 128, 128, False), ("bf16", 1400, 13, 3, 96, 48, True), ("mxfp8", 700, 64, 8, 256, 128, False),
+    ("mxfp8", 4100, 5, 2, 32, 32, True)])
+def test_qk_norm_rope_of_many_tokens(eg, fmt, T, hq, hkv, D, rot, inter):
+    """Enough tokens that a wave takes several of a token's passes, into the cache and without one."""
+    rng = np.random.default_rng(T)
+    row, qkv, qw, kw, pos, inv = rope_inputs(rng, T, hq, hkv, D, rot, 8, 5000)
+    ps = 16
+    pages = -(-T // ps) + 1
+    arrays, held, handle = make_cache(eg, rng, fmt, pages, hkv, ps, D)
+    slots = rng.permutation(pages * ps)[:T].astype(np.int64)
+    slots[[0, 4]] = [pages * ps, -1]
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k = Guarded((T, hq, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    q2, k2 = Guarded((T, hq, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    args = (qkv, hq, hkv, D, dev(qw), dev(kw), 1e-6, dev(pos), dev(inv), inter)
+    eg.engram_qk_norm_rope(*args, q.t, k.t, cache=handle, slots=dev(slots), bad_slots=bad)
+    eg.engram_qk_norm_rope(*args, q2.t, k2.t)
+    x = row[:, :(hq + 2 * hkv) * D].reshape(T, hq + 2 * hkv, D)
+    for got, xs, w in ((q, x[:, :hq], qw), (k, x[:, hq:hq + hkv], kw)):
+        want, mag = oa.qk_norm_rope(xs, w, 1e-6, pos, inv, inter)
+        within(got.host(), want, H * np.abs(want) + 2.0 ** -20 * mag + 1e-38)
+    assert np.array_equal(q.host(), q2.host()) and np.array_equal(k.host(), k2.host())
+    put(arrays, slots, k.host(), 0)
+    put(arrays, slots, x[:, hq + hkv:], 1)
+    same_cache(arrays, held)
+    assert bad.item() == 1
+
+
 # ---------------------------------------------------------------- attention
 
 def attend(eg, rng, fmt, ps, hq, hkv, D, lens, window=0, max_len=None, spoil=True, scale=None, sharp=2.0):
@@ -455,6 +517,45 @@ def test_cache_beyond_32_bit_offsets(eg, fmt):
     check_attention(out.host(), lse.host(), small, q, np.array([[0], [1]], np.int32), lens, 200, 0.0625, 0)
 
 
+def test_paged_attention_more_sequences_than_threads(eg):
+    """Many short sequences, empty ones among them, in equal runs that cut most of them."""
+    rng = np.random.default_rng(40)
+    lens = rng.integers(0, 700, size=700)
+    lens[rng.random(700) < 0.2] = 0
+    lens[[0, 1, -1]] = [0, 0, 0]
+    attend(eg, rng, "mxfp8", 8, 3, 1, 32, lens, max_len=1100)
+
+
+def test_paged_attention_one_long_among_short(eg):
+    rng = np.random.default_rng(41)
+    attend(eg, rng, "bf16", 16, 8, 2, 64, [3, 0, 20000, 1, 500, 129])
+    attend(eg, rng, "mxfp8", 32, 12, 3, 96, [1, 9000, 0, 4097, 128], window=4500)
+
+
+def test_paged_attention_many_head_blocks(eg):
+    """More query heads a key-value head than a workgroup takes, split over the length."""
+    attend(eg, np.random.default_rng(42), "bf16", 16, 70, 1, 64, [2000, 17, 0, 900])
+    attend(eg, np.random.default_rng(43), "mxfp8", 16, 66, 2, 192, [1500, 800])
+    attend(eg, np.random.default_rng(44), "bf16", 64, 33, 1, 256, [1500, 64])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_paged_attention_long_runs_of_shared_pages(eg, fmt):
+    """Runs longer than the pages held at a time; pages shared by all sequences."""
+    rng = np.random.default_rng(45)
+    n, ps, hq, D, pages = 40, 8, 2, 32, 50
+    arrays, held, handle = make_cache(eg, rng, fmt, pages, 1, ps, D)
+    lens = rng.integers(28000, 32000, size=n).astype(np.int32)
+    lens[5] = 0
+    table = rng.integers(0, pages, size=(n, 32000 // ps)).astype(np.int32)
+    q = bits(2.0 * rng.normal(size=(n, hq, D)))
+    out, lse = Guarded((n, hq, D), torch.int16), Guarded((n, hq), torch.float32)
+    ws = Guarded((eg.engram_paged_attention_workspace_bytes(n, hq, 1, D, 32000),), torch.uint8)
+    eg.engram_paged_attention(handle, dev(q), dev(table), dev(lens), 32000, 0.2, out.t, ws.t, lse=lse.t)
+    ws.host()
+    check_attention(out.host(), lse.host(), arrays, q, table, lens, 32000, 0.2, 0)
+
+
 # ---------------------------------------------------------------- the 4-bit weight
 
 def test_quantize_mxfp4(eg):
@@ -499,6 +600,40 @@ def test_project_mxfp4_many_columns_odd_scales(eg):
     eg.engram_project_mxfp4(dev(x), dev(codes), room[1:], out.t, T, K, N)
     want, mag = oa.project_mxfp4(x, codes, scales)
     within(out.host(), want, H * np.abs(want) + K * U * mag + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("K,N,shift", [(16640, 37, 0), (16640, 20, 1), (8224, 21, 0), (8320, 4, 2), (24608, 130, 3)])
+@pytest.mark.parametrize("T", [5, 70])
+def test_project_mxfp4_long_rows(eg, K, N, shift, T):
+    """Rows of more scales than are held at a time; scales at any address."""
+    rng = np.random.default_rng(K + T)
+    x = bits(rng.normal(size=(T, K)))
+    codes = rng.integers(0, 256, size=(N, K // 2), dtype=np.uint8)
+    scales = rng.integers(110, 130, size=(N, K // 32), dtype=np.uint8)
+    room = torch.empty(scales.size + shift, dtype=torch.uint8, device="cuda")
+    room[shift:] = dev(scales).flatten()
+    out = Guarded((T, N), torch.int16)
+    eg.engram_project_mxfp4(dev(x), dev(codes), room[shift:], out.t, T, K, N)
+    want, mag = oa.project_mxfp4(x, codes, scales)
+    within(out.host(), want, H * np.abs(want) + K * U * mag)
+
+
+def test_project_mxfp4_infinity_and_nan_stay_in_their_token(eg):
+    """K that ends inside a step of 128: an infinity of one token reaches no other."""
+    rng = np.random.default_rng(50)
+    T, K, N = 20, 160, 48
+    x = bits(rng.normal(size=(T, K)))
+    codes = rng.integers(0, 256, size=(N, K // 2), dtype=np.uint8)
+    scales = rng.integers(120, 130, size=(N, K // 32), dtype=np.uint8)
+    y = x.copy()
+    y[3, :] = 0x7F80
+    y[11, 0] = 0x7FC1
+    out, ref = Guarded((T, N), torch.int16), Guarded((T, N), torch.int16)
+    eg.engram_project_mxfp4(dev(x), dev(codes), dev(scales), ref.t, T, K, N)
+    eg.engram_project_mxfp4(dev(y), dev(codes), dev(scales), out.t, T, K, N)
+    others = np.setdiff1d(np.arange(T), [3, 11])
+    assert np.array_equal(out.host()[others], ref.host()[others])
+    assert not np.isfinite(oracle.bf16_value(out.host()[[3, 11]])).any()
 
 
 # ---------------------------------------------------------------- all of it together
