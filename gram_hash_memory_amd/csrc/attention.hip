@@ -80,7 +80,7 @@ struct Split {
   float2 *ml;
   int32_t *before;         // [n_seqs + 1], [n_seqs + 1] units of a run
   int32_t blocks, head_blocks, block_heads;
-  bool direct;
+  bool direct, two_buffers;  // the latter: of LDS for the waves' results
 };
 
 // How the head_dim = 32 * kDb dimensions fall to 16 lanes: pieces of 16, 8, 4,
@@ -154,8 +154,12 @@ struct Seen {
   int start, len, base, units;
 };
 __device__ __forceinline__ Seen seen_of(const PagedAttention &a, int64_t s) {
+  // Constant while the kernel runs: a uniform s is a scalar load, which does not
+  // wait for the vector loads in flight.
+  typedef const int32_t __attribute__((address_space(4))) *Constant;
   const int64_t room = int64_t(a.table_width) << a.cache.page_shift;
-  const int len = int(min(int64_t(min(max(a.lens[s], 0), a.max_len)), room));
+  const int stated = reinterpret_cast<Constant>(reinterpret_cast<uintptr_t>(a.lens))[s];
+  const int len = int(min(int64_t(min(max(stated, 0), a.max_len)), room));
   const int start = a.window > 0 ? max(0, len - a.window) : 0;
   const int base = start / kTile * kTile;
   return {start, len, base, int((int64_t(len) - base + kUnit - 1) / kUnit)};
@@ -220,14 +224,26 @@ __device__ __forceinline__ Run run_of(const PagedAttention &a, const Split &sp, 
   return {run_lds[0], run_lds[1], int(min(int64_t(per), total - u0))};
 }
 
+// What a workgroup works at: places c0 .. c1 - 1, a stretch of a piece (the
+// units of a pair that its run holds), whose pages LDS has room for.
+struct Work {
+  Seen seen;
+  int s, pair, kvh, hb, index;             // index: which piece of the run
+  int end, c0, c1, tiles, page0, pages;
+  bool whole, first;                       // the piece is its whole pair; the stretch begins it
+};
+
 template <int kDb, bool kMx, int kHt>
 __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attention_kernel(
     PagedAttention a, Split sp) {
   constexpr int D = 32 * kDb, kRowBytes = kMx ? D : 2 * D, kAcc = D / 16;
+  constexpr int kPageRegs = (kMaxChunk / kMinPage + 1 + 64 * kW - 1) / (64 * kW);
   using P = Pieces<kDb>;
-  __shared__ int64_t page_lds[kMaxChunk / kMinPage + 1];   // a page's first row, or -1
-  __shared__ float2 ml_lds[kW][kHt][16];
-  extern __shared__ f32x4 o_lds[];                         // [kW - 1][kAcc][4][heads of a tile]
+  // Two of each: the next stretch's are written while this one's are in use.
+  __shared__ int64_t page_lds[2][kMaxChunk / kMinPage + 1];   // a page's first row, or -1
+  __shared__ int bad_lds[2][kW];
+  __shared__ float2 ml_lds[2][kW][kHt][16];
+  extern __shared__ f32x4 o_lds[];           // [1 or 2][kW - 1][kAcc][4][heads of a tile]
 
   const CacheView &c = a.cache;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -241,83 +257,112 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
   run.s = __builtin_amdgcn_readfirstlane(run.s);
   run.local = __builtin_amdgcn_readfirstlane(run.local);
   run.left = __builtin_amdgcn_readfirstlane(run.left);
-  for (int piece = 0; run.left > 0; ++piece) {
-  const int s = run.s;
-  const Seen seen = seen_of(a, s);
-  if (seen.units == 0 && !sp.direct) {
-    ++run.s;
-    --piece;
-    continue;
-  }
-  // Units first .. first + count - 1 of the pair.
-  const int pair = sp.direct ? int(blockIdx.x % pairs) : run.local / seen.units;
-  const int first_unit = sp.direct ? 0 : run.local - pair * seen.units;
-  const int count = sp.direct ? seen.units : min(seen.units - first_unit, run.left);
-  const bool whole_pair = count == seen.units;
-  run.left -= sp.direct ? 1 : count;
-  run.local += count;
-  if (run.local == seen.units * pairs) ++run.s, run.local = 0;
 
-  const int kvh = pair / sp.head_blocks, hb = pair - kvh * sp.head_blocks;
-  const int heads = min(16 * kHt, group - hb * kHeadBlock);   // here; kHt = 1 only for up to 16
-  const int64_t row0 = int64_t(s) * a.q_heads + kvh * group + hb * kHeadBlock;
-  const int begin = seen.base + first_unit * kUnit;
-  const int end = int(min(int64_t(seen.len), int64_t(begin) + int64_t(count) * kUnit));
+  auto next_work = [&](Work &w) {
+    if (w.c1 < w.end) {
+      w.c0 = w.c1;
+      w.first = false;
+    } else {
+      for (;; ++run.s) {
+        if (run.left <= 0) return false;
+        w.seen = seen_of(a, run.s);
+        if (sp.direct || w.seen.units > 0) break;
+      }
+      w.s = run.s;
+      w.pair = sp.direct ? int(blockIdx.x % pairs) : run.local / w.seen.units;
+      const int unit = sp.direct ? 0 : run.local - w.pair * w.seen.units;
+      const int count = sp.direct ? w.seen.units : min(w.seen.units - unit, run.left);
+      run.left -= sp.direct ? 1 : count;
+      run.local += count;
+      if (run.local == w.seen.units * pairs) ++run.s, run.local = 0;
+      w.whole = count == w.seen.units;
+      w.first = true;
+      ++w.index;
+      w.kvh = w.pair / sp.head_blocks;
+      w.hb = w.pair - w.kvh * sp.head_blocks;
+      w.c0 = w.seen.base + unit * kUnit;
+      w.end = int(min(int64_t(w.seen.len), int64_t(w.c0) + int64_t(count) * kUnit));
+    }
+    w.c1 = min(w.end, w.c0 + kMaxChunk);
+    w.tiles = (w.c1 - w.c0 + kTile - 1) / kTile;
+    w.page0 = w.c0 >> c.page_shift;
+    w.pages = ((w.c0 + max(1, w.tiles) * kTile - 1) >> c.page_shift) - w.page0 + 1;
+    return true;
+  };
+
+  // The pages of a stretch: requested into registers, later put in LDS.
+  auto shown_page = [&](const Work &w, int e) {
+    const int first = (w.page0 + e) << c.page_shift;
+    return e < w.pages && first < w.c1 && first + mask >= w.seen.start;
+  };
+  auto ask_pages = [&](const Work &w, int(&page)[kPageRegs]) {
+#pragma unroll
+    for (int k = 0; k < kPageRegs; ++k) {
+      const int e = threadIdx.x + k * 64 * kW;
+      page[k] = -1;
+      if (shown_page(w, e)) page[k] = a.table[int64_t(w.s) * a.table_width + w.page0 + e];
+    }
+  };
+  auto put_pages = [&](const Work &w, const int(&page)[kPageRegs], int buf) {
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kPageRegs; ++k) {
+      const int e = threadIdx.x + k * 64 * kW;
+      if (e >= w.pages) break;
+      const bool in = page[k] >= 0 && page[k] < c.pages;
+      bad |= !in && shown_page(w, e);
+      page_lds[buf][e] = in ? (int64_t(page[k]) * c.kv_heads + w.kvh) << c.page_shift : -1;
+    }
+    if (bad && w.pair == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
+    const bool any = __any(bad);
+    if (lane == 0) bad_lds[buf][wave] = any;
+  };
+  // LDS written by all, read by all; loads stay in flight.
+  auto barrier = [&] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto bad_of = [&](int buf) {
+    int any = 0;
+#pragma unroll
+    for (int x = 0; x < kW; ++x) any |= bad_lds[buf][x];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
+  };
 
   // Query heads as B operands: lane l holds 8 dimensions of head l % 16 a step.
   // In the 8-bit format a lane's 16 bytes of K are two steps.
   bf16x8 q[kHt][kDb];
+  auto heads_of = [&](const Work &w) {             // kHt = 1 only for up to 16
+    return min(16 * kHt, group - w.hb * kHeadBlock);
+  };
+  auto row0_of = [&](const Work &w) {
+    return int64_t(w.s) * a.q_heads + w.kvh * group + w.hb * kHeadBlock;
+  };
+  auto load_q = [&](const Work &w) {
+    const int heads = heads_of(w);
+    const uint16_t *src = a.q + row0_of(w) * D;
 #pragma unroll
-  for (int t = 0; t < kHt; ++t)
+    for (int t = 0; t < kHt; ++t)
 #pragma unroll
-    for (int kk = 0; kk < kDb; ++kk) {
-      const int d = kMx && (kk | 1) < kDb ? 64 * (kk / 2) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
-      // Columns past the last head repeat it; nothing reads their results.
-      q[t][kk] = __builtin_bit_cast(
-          bf16x8, *reinterpret_cast<const u32x4 *>(
-                      a.q + (row0 + min(16 * t + col, heads - 1)) * D + d));
-    }
-
-  float m[kHt], l[kHt];
-  f32x4 o[kHt][kAcc];
-#pragma unroll
-  for (int t = 0; t < kHt; ++t) {
-    m[t] = -INFINITY, l[t] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kAcc; ++n) o[t][n] = f32x4{};
-  }
-
-  for (int c0 = begin; c0 < end; c0 += kMaxChunk) {
-  const int c1 = int(min(int64_t(end), int64_t(c0) + kMaxChunk));
-  const int tiles = (c1 - c0 + kTile - 1) / kTile;
-
-  // The pages of these places.
-  const int page0 = c0 >> c.page_shift;
-  const int pages = int((int64_t(c0) + tiles * kTile - 1) >> c.page_shift) - page0 + 1;
-  bool bad = false;
-  if (c0 > begin) __syncthreads();             // the pages before are in use up to here
-  for (int e = threadIdx.x; e < pages; e += 64 * kW) {
-    const int64_t first = int64_t(page0 + e) << c.page_shift;
-    int64_t row = -1;
-    if (first < c1 && first + mask >= seen.start) {
-      const int page = a.table[int64_t(s) * a.table_width + page0 + e];
-      if (page >= 0 && page < c.pages) row = (int64_t(page) * c.kv_heads + kvh) << c.page_shift;
-      else bad = true;
-    }
-    page_lds[e] = row;
-  }
-  if (bad && pair == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
-  const bool any_bad = __syncthreads_or(bad);
+      for (int kk = 0; kk < kDb; ++kk) {
+        const int d = kMx && (kk | 1) < kDb ? 64 * (kk / 2) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
+        // Columns past the last head repeat it; nothing reads their results.
+        q[t][kk] = __builtin_bit_cast(
+            bf16x8, *reinterpret_cast<const u32x4 *>(src + min(16 * t + col, heads - 1) * D + d));
+      }
+  };
 
   Held<kDb, kMx> held;
-  auto row_of = [&](int p) {
-    const int64_t r = page_lds[(p >> c.page_shift) - page0];
+  auto row_of = [&](const Work &w, int buf, int p) {
+    const int64_t r = page_lds[buf][(p >> c.page_shift) - w.page0];
     return (r < 0 ? 0 : r) + (p & mask);       // a page that is not seen: rows of page 0 instead
   };
-  auto load_k = [&](int tile) {
+  auto load_k = [&](const Work &w, int buf, int tile) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t row = row_of(c0 + kTile * tile + 16 * u + col);
+      const int64_t row = row_of(w, buf, w.c0 + kTile * tile + 16 * u + col);
       const uint8_t *src = static_cast<const uint8_t *>(c.k) + row * kRowBytes;
       if constexpr (!kMx) {
 #pragma unroll
@@ -336,218 +381,279 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
       }
     }
   };
-  auto load_v = [&](int tile) {
+  auto load_v = [&](const Work &w, int buf, int tile) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t row = row_of(c0 + kTile * tile + 16 * u + 4 * g);
+      const int64_t row = row_of(w, buf, w.c0 + kTile * tile + 16 * u + 4 * g);
       const uint8_t *src = static_cast<const uint8_t *>(c.v) + row * kRowBytes;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         each_piece<P::kN>([&](auto piece) {
-          constexpr int w = P::width(piece.value), first = P::base(piece.value);
+          constexpr int wd = P::width(piece.value), first = P::base(piece.value);
           if constexpr (kMx) {
-            load_bytes<w>(&held.v[4 * u + j][first / 64], src + j * kRowBytes + first + w * col);
-            held.vs[4 * u + j][piece.value] = c.v_scales[(row + j) * kDb + (first + w * col) / 32];
+            load_bytes<wd>(&held.v[4 * u + j][first / 64], src + j * kRowBytes + first + wd * col);
+            held.vs[4 * u + j][piece.value] = c.v_scales[(row + j) * kDb + (first + wd * col) / 32];
           } else {
-            load_bytes<2 * w>(&held.v[4 * u + j][first / 32],
-                              src + j * kRowBytes + 2 * (first + w * col));
+            load_bytes<2 * wd>(&held.v[4 * u + j][first / 32],
+                              src + j * kRowBytes + 2 * (first + wd * col));
           }
         });
       }
     }
   };
 
-  // The loads are issued without a condition (the last ones for nothing, from
-  // the cache): a wave then waits for no more of them than it needs.
-  if (wave < tiles) {
-    int tile = wave;
-    load_k(tile);
-    __builtin_amdgcn_sched_barrier(0);
-    load_v(tile);
-    do {
-      const int next = min(tile + kW, tiles - 1);
-      const int p0 = c0 + kTile * tile;
-      f32x4 z[kHt][2];
+  float m[kHt], l[kHt];
+  f32x4 o[kHt][kAcc];
+  auto reset = [&] {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+    for (int t = 0; t < kHt; ++t) {
+      m[t] = -INFINITY, l[t] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < kHt; ++t) z[t][u] = f32x4{};
-#pragma unroll
-        for (int kk = 0; kk < kDb; ++kk) {
-          bf16x8 f;
-          if constexpr (kMx) {
-            const uint32_t *w = &held.k[u][2 * kk];
-            const float sc = __uint_as_float(held.ks[u][kk / 2] << 23);
-            f = as_frag(mx_pair(w[0], sc, false), mx_pair(w[0], sc, true), mx_pair(w[1], sc, false),
-                        mx_pair(w[1], sc, true));
-          } else {
-            const uint32_t *w = &held.k[u][4 * kk];
-            f = as_frag(w[0], w[1], w[2], w[3]);
-          }
-#pragma unroll
-          for (int t = 0; t < kHt; ++t)
-            z[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][kk], z[t][u], 0, 0, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      load_k(next);
-      __builtin_amdgcn_sched_barrier(0);
-      // Bits 4 u + r: place 16 u + 4 g + r of the tile is seen.  The values of
-      // others, which may be anything, count as 0 (times a scale that is finite).
-      const bool whole = !any_bad && p0 >= seen.start && p0 + kTile <= seen.len;
-      uint32_t shown = 0xFF;
-      if (!whole) {
-        shown = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int p = p0 + 16 * u + 4 * g;
-          const bool page = page_lds[(p >> c.page_shift) - page0] >= 0;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (page && p + r >= seen.start && p + r < seen.len) shown |= 1u << (4 * u + r);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < int(sizeof(held.v[0]) / 4); ++i)
-            held.v[j][i] = shown >> j & 1 ? held.v[j][i] : 0;
-      }
+      for (int n = 0; n < kAcc; ++n) o[t][n] = f32x4{};
+    }
+  };
+  reset();
 
-      bf16x8 w[kHt];                             // the weights, as B operands
+  // A piece's parts, the waves' results, to LDS; then joined by wave 0, in wave order.
+  auto part_lds = [&](const Work &w) {
+    return o_lds + (sp.two_buffers ? (w.index & 1) * (kW - 1) * kAcc * 4 * min(16, heads_of(w)) : 0);
+  };
+  auto give = [&](const Work &w, int t, int here) {
+    f32x4 *const ob = part_lds(w);
+    if (wave > 0 && col < here) {
 #pragma unroll
-      for (int t = 0; t < kHt; ++t) {
-        float e[8];
+      for (int n = 0; n < kAcc; ++n) ob[((wave - 1) * kAcc + n) * 4 * here + g * here + col] = o[t][n];
+    }
+  };
+  auto join = [&](const Work &w) {
+    const int heads = heads_of(w);
+    const f32x4 *const ob = part_lds(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = z[t][j / 4][j % 4] * to_log2;
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = shown >> j & 1 ? e[j] : -INFINITY;
-        }
-        float top = e[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) top = fmaxf(top, e[j]);
-        top = column_max(top);
-        if (__any(top > m[t])) {                 // rarely after the first tiles
-          const float mn = fmaxf(m[t], top);
-          const float keep = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
-          m[t] = mn;
-          l[t] *= keep;
-#pragma unroll
-          for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
-        }
-        const float ms = m[t] == -INFINITY ? 0.0f : m[t];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          e[j] = __builtin_amdgcn_exp2f(e[j] - ms);
-          sum += e[j];
-        }
-        l[t] += sum;
-        // Rounded to bf16 for the matrix cores; the sum is of the fp32 ones.
-        w[t] = as_frag(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                       pack_bf16x2(e[6], e[7]));
+    for (int t = 0; t < kHt; ++t) {
+      const int here = min(16, heads - 16 * t);
+      if (here <= 0) break;
+      if (t > 0) {
+        barrier();
+        give(w, t, here);
+        barrier();
       }
-
+      if (wave > 0 || col >= here) continue;
+      float top = m[t];
+#pragma unroll
+      for (int x = 1; x < kW; ++x) top = fmaxf(top, ml_lds[w.index & 1][x][t][col].x);
+      const float ms = top == -INFINITY ? 0.0f : top;
+      float keep = __builtin_amdgcn_exp2f(m[t] - ms), sum = l[t] * keep;
+#pragma unroll
+      for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
+#pragma unroll 1
+      for (int x = 1; x < kW; ++x) {
+        const float2 ml = ml_lds[w.index & 1][x][t][col];
+        keep = __builtin_amdgcn_exp2f(ml.x - ms);
+        sum += ml.y * keep;
+#pragma unroll
+        for (int n = 0; n < kAcc; ++n)
+          o[t][n] += ob[((x - 1) * kAcc + n) * 4 * here + g * here + col] * keep;
+      }
+      const int64_t row = row0_of(w) + 16 * t + col;
+      // A run's first piece, or a later one (the run's last) that it does not hold whole.
+      const int64_t part = (2 * int64_t(blockIdx.x) + (w.index > 0)) * sp.block_heads + 16 * t + col;
+      const float inv = !w.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (g == 0) {
+        if (!w.whole) sp.ml[part] = float2{top, sum};
+        else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      }
       each_piece<P::kN>([&](auto piece) {
         constexpr int wd = P::width(piece.value), first = P::base(piece.value);
 #pragma unroll
-        for (int i = 0; i < wd / 2; ++i) {
-          uint32_t x[8];                   // dimensions 2 i, 2 i + 1 of the lane's 8 places
+        for (int r = 0; r < 4; ++r) {
+          const int d = first + wd * (4 * g + r);
+          if (w.whole) {
+            uint16_t *dst = a.out + row * D + d;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if constexpr (kMx)
-              x[j] = mx_pair(held.v[j][first / 64 + i / 2],
-                             __uint_as_float(min(held.vs[j][piece.value], 254u) << 23), i & 1);
-            else
-              x[j] = held.v[j][first / 32 + i];
-          }
-          const bf16x8 even = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u),
-                                      __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
-                                      __builtin_amdgcn_perm(x[5], x[4], 0x05040100u),
-                                      __builtin_amdgcn_perm(x[7], x[6], 0x05040100u));
-          const bf16x8 odd = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u),
-                                     __builtin_amdgcn_perm(x[3], x[2], 0x07060302u),
-                                     __builtin_amdgcn_perm(x[5], x[4], 0x07060302u),
-                                     __builtin_amdgcn_perm(x[7], x[6], 0x07060302u));
-          const int n = first / 16 + 2 * i;
+            for (int i = 0; i < wd / 2; ++i)
+              reinterpret_cast<uint32_t *>(dst)[i] = pack_bf16x2(
+                  o[t][first / 16 + 2 * i][r] * inv, o[t][first / 16 + 2 * i + 1][r] * inv);
+          } else {
+            float *dst = sp.o + part * D + d;
 #pragma unroll
-          for (int t = 0; t < kHt; ++t) {
-            o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, w[t], o[t][n], 0, 0, 0);
-            o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, w[t], o[t][n + 1], 0, 0, 0);
+            for (int i = 0; i < wd; ++i) dst[i] = o[t][first / 16 + i][r];
           }
         }
       });
-      __builtin_amdgcn_sched_barrier(0);
-      load_v(next);
-      __builtin_amdgcn_sched_barrier(0);
-    } while ((tile += kW) < tiles);
-  }
+    }
+    reset();
+    if (!sp.two_buffers) barrier();
+  };
 
-  }
+  Work w{};
+  w.index = -1;
+  if (!next_work(w)) return;
+  int page[kPageRegs];
+  ask_pages(w, page);
+  put_pages(w, page, 0);
+  barrier();
+  // A stretch's first loads; then, while they fly, the join of the piece before
+  // it and the pages of the one after it.  Loads are issued without a condition
+  // (a stretch's last ones for nothing, from the cache): a wave then waits for
+  // no more of them than it needs.
+  Work before{};
+  bool join_before = false;
+  for (int buf = 0;; buf ^= 1) {
+    load_q(w);
+    __builtin_amdgcn_sched_barrier(0);
+    load_k(w, buf, max(0, min(wave, w.tiles - 1)));
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(w, buf, max(0, min(wave, w.tiles - 1)));
+    __builtin_amdgcn_sched_barrier(0);
+    if (join_before) join(before);
+    const bool any_bad = bad_of(buf);
+    Work nw = w;
+    const bool more = next_work(nw);
+    if (more) ask_pages(nw, page);
+    // q waited for here, once, and not in the loop, which would do so each time.
+#pragma unroll
+    for (int t = 0; t < kHt; ++t)
+#pragma unroll
+      for (int kk = 0; kk < kDb; ++kk) asm volatile("" : "+v"(q[t][kk]));
 
-  // The waves' results joined by wave 0, in wave order.
+    if (wave < w.tiles) {
+      int tile = wave;
+      do {
+        const int next = min(tile + kW, w.tiles - 1);
+        const int p0 = w.c0 + kTile * tile;
+        f32x4 z[kHt][2];
 #pragma unroll
-  for (int t = 0; t < kHt; ++t) {
-    l[t] = column_sum(l[t]);
-    if (g == 0) ml_lds[wave][t][col] = float2{m[t], l[t]};
-  }
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-  for (int t = 0; t < kHt; ++t) {
-    const int here = min(16, heads - 16 * t);
-    if (here <= 0) break;
-    const bool on = col < here;
-    if (t > 0) __syncthreads();
-    if (wave > 0 && on) {
+          for (int t = 0; t < kHt; ++t) z[t][u] = f32x4{};
 #pragma unroll
-      for (int n = 0; n < kAcc; ++n)
-        o_lds[((wave - 1) * kAcc + n) * 4 * here + g * here + col] = o[t][n];
-    }
-    __syncthreads();
-    if (wave > 0 || !on) continue;
-    float top = m[t];
+          for (int kk = 0; kk < kDb; ++kk) {
+            bf16x8 f;
+            if constexpr (kMx) {
+              const uint32_t *w = &held.k[u][2 * kk];
+              const float sc = __uint_as_float(held.ks[u][kk / 2] << 23);
+              f = as_frag(mx_pair(w[0], sc, false), mx_pair(w[0], sc, true), mx_pair(w[1], sc, false),
+                          mx_pair(w[1], sc, true));
+            } else {
+              const uint32_t *w = &held.k[u][4 * kk];
+              f = as_frag(w[0], w[1], w[2], w[3]);
+            }
 #pragma unroll
-    for (int x = 1; x < kW; ++x) top = fmaxf(top, ml_lds[x][t][col].x);
-    const float ms = top == -INFINITY ? 0.0f : top;
-    float keep = __builtin_amdgcn_exp2f(m[t] - ms), sum = l[t] * keep;
-#pragma unroll
-    for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
-#pragma unroll 1
-    for (int x = 1; x < kW; ++x) {
-      const float2 ml = ml_lds[x][t][col];
-      keep = __builtin_amdgcn_exp2f(ml.x - ms);
-      sum += ml.y * keep;
-#pragma unroll
-      for (int n = 0; n < kAcc; ++n)
-        o[t][n] += o_lds[((x - 1) * kAcc + n) * 4 * here + g * here + col] * keep;
-    }
-    const int64_t row = row0 + 16 * t + col;
-    // A run's first piece, or a later one (the run's last) that it does not hold whole.
-    const int64_t part = (2 * int64_t(blockIdx.x) + (piece > 0)) * sp.block_heads + 16 * t + col;
-    const float inv = !whole_pair ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (g == 0) {
-      if (!whole_pair) sp.ml[part] = float2{top, sum};
-      else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-    }
-    each_piece<P::kN>([&](auto piece) {
-      constexpr int wd = P::width(piece.value), first = P::base(piece.value);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = first + wd * (4 * g + r);
-        if (whole_pair) {
-          uint16_t *dst = a.out + row * D + d;
-#pragma unroll
-          for (int i = 0; i < wd / 2; ++i)
-            reinterpret_cast<uint32_t *>(dst)[i] = pack_bf16x2(
-                o[t][first / 16 + 2 * i][r] * inv, o[t][first / 16 + 2 * i + 1][r] * inv);
-        } else {
-          float *dst = sp.o + part * D + d;
-#pragma unroll
-          for (int i = 0; i < wd; ++i) dst[i] = o[t][first / 16 + i][r];
+            for (int t = 0; t < kHt; ++t)
+              z[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][kk], z[t][u], 0, 0, 0);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(w, buf, next);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // Bits 4 u + r: place 16 u + 4 g + r of the tile is seen.  The values of
+        // others, which may be anything, count as 0 (times a scale that is finite).
+        const bool whole = !any_bad && p0 >= w.seen.start && p0 + kTile <= w.seen.len;
+        uint32_t shown = 0xFF;
+        if (!whole) {
+          shown = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int p = p0 + 16 * u + 4 * g;
+            const bool page = page_lds[buf][(p >> c.page_shift) - w.page0] >= 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (page && p + r >= w.seen.start && p + r < w.seen.len) shown |= 1u << (4 * u + r);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < int(sizeof(held.v[0]) / 4); ++i)
+              held.v[j][i] = shown >> j & 1 ? held.v[j][i] : 0;
+        }
+
+        bf16x8 wt[kHt];                             // the weights, as B operands
+#pragma unroll
+        for (int t = 0; t < kHt; ++t) {
+          float e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = z[t][j / 4][j % 4] * to_log2;
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = shown >> j & 1 ? e[j] : -INFINITY;
+          }
+          float top = e[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) top = fmaxf(top, e[j]);
+          top = column_max(top);
+          if (__any(top > m[t])) {                 // rarely after the first tiles
+            const float mn = fmaxf(m[t], top);
+            const float keep = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+            m[t] = mn;
+            l[t] *= keep;
+#pragma unroll
+            for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
+          }
+          const float ms = m[t] == -INFINITY ? 0.0f : m[t];
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            e[j] = __builtin_amdgcn_exp2f(e[j] - ms);
+            sum += e[j];
+          }
+          l[t] += sum;
+          // Rounded to bf16 for the matrix cores; the sum is of the fp32 ones.
+          wt[t] = as_frag(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                         pack_bf16x2(e[6], e[7]));
+        }
+
+        each_piece<P::kN>([&](auto piece) {
+          constexpr int wd = P::width(piece.value), first = P::base(piece.value);
+#pragma unroll
+          for (int i = 0; i < wd / 2; ++i) {
+            uint32_t x[8];                   // dimensions 2 i, 2 i + 1 of the lane's 8 places
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (kMx)
+                x[j] = mx_pair(held.v[j][first / 64 + i / 2],
+                               __uint_as_float(min(held.vs[j][piece.value], 254u) << 23), i & 1);
+              else
+                x[j] = held.v[j][first / 32 + i];
+            }
+            const bf16x8 even = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u),
+                                        __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
+                                        __builtin_amdgcn_perm(x[5], x[4], 0x05040100u),
+                                        __builtin_amdgcn_perm(x[7], x[6], 0x05040100u));
+            const bf16x8 odd = as_frag(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u),
+                                       __builtin_amdgcn_perm(x[3], x[2], 0x07060302u),
+                                       __builtin_amdgcn_perm(x[5], x[4], 0x07060302u),
+                                       __builtin_amdgcn_perm(x[7], x[6], 0x07060302u));
+            const int n = first / 16 + 2 * i;
+#pragma unroll
+            for (int t = 0; t < kHt; ++t) {
+              o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, wt[t], o[t][n], 0, 0, 0);
+              o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, wt[t], o[t][n + 1], 0, 0, 0);
+            }
+          }
+        });
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(w, buf, next);
+        __builtin_amdgcn_sched_barrier(0);
+      } while ((tile += kW) < w.tiles);
+    }
+
+    if (w.c1 == w.end) {                           // the end of a piece
+#pragma unroll
+      for (int t = 0; t < kHt; ++t) {
+        l[t] = column_sum(l[t]);
+        if (g == 0) ml_lds[w.index & 1][wave][t][col] = float2{m[t], l[t]};
       }
-    });
+      give(w, 0, min(16, heads_of(w)));
+    }
+    if (more) put_pages(nw, page, buf ^ 1);
+    barrier();
+    if (!more) break;
+    join_before = w.c1 == w.end;
+    before = w;
+    w = nw;
   }
-  }
+  join(w);
 }
 
 // A pair's pieces to its result, in order: one workgroup per (sequence, query
@@ -611,8 +717,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Sp
 }
 
 template <int kDb, bool kMx>
-void by_heads(const PagedAttention &a, const Split &sp, hipStream_t stream) {
-  const unsigned lds = unsigned((kW - 1) * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
+void by_heads(const PagedAttention &a, Split sp, hipStream_t stream) {
+  unsigned lds = unsigned((kW - 1) * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
+  sp.two_buffers = 2 * lds <= 49152;             // 64 KB with the rest
+  if (sp.two_buffers) lds *= 2;
   const dim3 grid(sp.blocks), block(64 * kW);
   if (sp.block_heads > 16)
     hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, 2>), grid, block, lds, stream, a, sp);
