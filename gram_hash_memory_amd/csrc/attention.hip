@@ -658,10 +658,10 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
 
 // A pair's pieces to its result, in order: one workgroup per (sequence, query
 // head), D / 4 lanes a piece.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 64;
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Split sp) {
   __shared__ f32x4 part_lds[kJoinThreads];
-  __shared__ float top_lds[kJoinThreads / 64], sum_lds[kJoinThreads / 64];
+  __shared__ float2 ml_lds[kJoinThreads / 8];
   const int D = a.cache.head_dim, lanes = D / 4;
   const int64_t row = blockIdx.x;
   const int s = int(row / a.q_heads), h = int(row - int64_t(s) * a.q_heads);
@@ -675,42 +675,41 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Sp
   if (parts == 1) return;                          // its run has written the result
   // The first run holds the pair's beginning: as its first piece, or its last.
   const int64_t at0 = int64_t(in_group - hb * kHeadBlock);
-  auto part_of = [&](int i) {
-    return (2 * int64_t(r0 + i) + (i == 0 && int64_t(r0) * per < u0)) * sp.block_heads + at0;
-  };
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads) top = fmaxf(top, sp.ml[part_of(i)].x);
-  for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-  if (lane == 0) top_lds[wave] = top;
-  __syncthreads();
-  for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, top_lds[w]);
-  const float ms = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-    const float2 ml = sp.ml[part_of(i)];
-    sum += ml.y * __builtin_amdgcn_exp2f(ml.x - ms);
-  }
-  for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
-  if (lane == 0) sum_lds[wave] = sum;
-
+  // Each group of D / 4 lanes takes every rows-th piece; the groups' results are
+  // joined in their order.
   const int rows = kJoinThreads / lanes, mine = threadIdx.x / lanes, at = threadIdx.x % lanes;
   f32x4 o{};
+  float m = -INFINITY, l = 0.0f;
   if (mine < rows) {
-    const f32x4 *src = reinterpret_cast<const f32x4 *>(sp.o) + at;
+#pragma unroll 4
     for (int i = mine; i < parts; i += rows) {
-      const int64_t part = part_of(i);
-      o += src[part * lanes] * __builtin_amdgcn_exp2f(sp.ml[part].x - ms);
+      const int64_t part = (2 * int64_t(r0 + i) + (i == 0 && int64_t(r0) * per < u0)) * sp.block_heads + at0;
+      const float2 ml = sp.ml[part];
+      const f32x4 v = reinterpret_cast<const f32x4 *>(sp.o)[part * lanes + at];
+      const float top = fmaxf(m, ml.x), ms = top == -INFINITY ? 0.0f : top;
+      const float keep = __builtin_amdgcn_exp2f(m - ms), add = __builtin_amdgcn_exp2f(ml.x - ms);
+      o = o * keep + v * add;
+      l = l * keep + ml.y * add;
+      m = top;
     }
     part_lds[threadIdx.x] = o;
+    if (at == 0) ml_lds[mine] = float2{m, l};
   }
   __syncthreads();
-  sum = 0.0f;
-  for (int w = 0; w < kJoinThreads / 64; ++w) sum += sum_lds[w];
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
   if (mine != 0) return;
-  for (int w = 1; w < rows; ++w) o += part_lds[w * lanes + at];
+  float top = m;
+  for (int w = 1; w < rows; ++w) top = fmaxf(top, ml_lds[w].x);
+  const float ms = top == -INFINITY ? 0.0f : top;
+  float keep = __builtin_amdgcn_exp2f(m - ms), sum = l * keep;
+  o *= keep;
+  for (int w = 1; w < rows; ++w) {
+    const float2 ml = ml_lds[w];
+    keep = __builtin_amdgcn_exp2f(ml.x - ms);
+    sum += ml.y * keep;
+    o += part_lds[w * lanes + at] * keep;
+  }
+  if (at == 0 && a.lse)
+    a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   reinterpret_cast<u32x2 *>(a.out + row * D)[at] =
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
