@@ -50,10 +50,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int64_t kBlocks = 256;
 
 // Up to 4 units (512 places) the join costs more than it saves (one stream of
-// 300 places: 8.3 us against 11.3 us); up to 8 where the pairs fill the CUs on
-// their own (64 streams of up to 1000: 36.9 against 46 us; one stream of 1000:
-// 13.9 against 11.3 us).
-inline int64_t direct_units(int64_t pairs) { return pairs >= kBlocks ? 8 : 4; }
+// 300 places: 8.4 us against 10.7 us; of 1000: 13.9 against 10.5 us).  Where the
+// pairs fill the CUs on their own, up to 16 units and some 540 KB a pair, what a
+// workgroup streams in the time that dealing out and joining take (64 streams
+// of up to 1000 places in bf16: 36.7 against 43.2 us; 32 of up to 2000 in 8 bits
+// 23.6 against 29.4, in bf16, 40 of them, 53.5 against 46.3 us).
+inline int64_t direct_units(int64_t pairs, int64_t unit_bytes) {
+  return pairs < kBlocks ? 4 : std::max<int64_t>(4, std::min<int64_t>(16, 544 * 1024 / unit_bytes));
+}
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -63,12 +67,14 @@ struct Plan {
   bool direct;
 };
 
-Plan plan_for(int n_seqs, int q_heads, int kv_heads, int max_len) {
+// span: the places seen at most, from a multiple of kTile on.  row_bytes: of a
+// key or a value.
+Plan plan_for(int n_seqs, int q_heads, int kv_heads, int64_t span, int64_t row_bytes) {
   Plan p{};
   p.head_blocks = int(ceil_div(q_heads / kv_heads, kHeadBlock));
   p.pairs = int64_t(n_seqs) * kv_heads * p.head_blocks;
-  p.units = std::max<int64_t>(1, ceil_div(max_len, kUnit));
-  p.direct = p.units <= direct_units(p.pairs);
+  p.units = std::max<int64_t>(1, ceil_div(span, kUnit));
+  p.direct = p.units <= direct_units(p.pairs, 2 * kUnit * row_bytes);
   p.blocks = p.direct ? p.pairs : std::min(kBlocks, p.pairs * p.units);
   return p;
 }
@@ -738,13 +744,14 @@ inline int block_heads(int q_heads, int kv_heads) { return std::min(kHeadBlock, 
 }  // namespace
 
 int64_t paged_attention_units(int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len) {
-  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len);
+  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len, 1);
   return p.pairs * p.units;
 }
 
 int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
                                   int32_t head_dim, int32_t max_len) {
-  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len);
+  // As for bf16, without a window: other calls take no more workgroups.
+  const Plan p = plan_for(n_seqs, q_heads, kv_heads, max_len, 2 * head_dim);
   if (p.direct) return 0;
   const int64_t parts = 2 * p.blocks * block_heads(q_heads, kv_heads);
   return (parts * (head_dim + 2) + n_seqs + 2) * int64_t(sizeof(float));
@@ -752,7 +759,9 @@ int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_he
 
 hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream) {
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
-  const Plan p = plan_for(a.n_seqs, a.q_heads, hkv, a.max_len);
+  const int64_t row_bytes = a.cache.k_scales ? D + D / 32 : 2 * D;
+  const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_len, int64_t(a.window) + kTile - 1) : a.max_len;
+  const Plan p = plan_for(a.n_seqs, a.q_heads, hkv, span, row_bytes);
   Split sp{};
   sp.blocks = int32_t(p.blocks);
   sp.head_blocks = p.head_blocks;
