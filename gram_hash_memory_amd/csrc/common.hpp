@@ -178,7 +178,7 @@ struct QkRope {
   // From qk_rope_plan: the heads a token has here (the values' ones with a
   // cache), and how the waves share them.
   float inv_dim;
-  int32_t heads, passes_per_wave, waves_per_token;
+  int32_t heads, passes_per_wave, q_waves, waves_per_token;
 };
 int64_t qk_rope_plan(QkRope *a);            // workgroups
 hipError_t launch_qk_norm_rope(const QkRope &a, bool interleaved, int64_t blocks,
