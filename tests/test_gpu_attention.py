@@ -716,6 +716,20 @@ def test_step_on_another_stream_and_in_a_graph(eg):
         assert np.array_equal(eager, host(s["y"]))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
+def test_example_of_a_prompt_and_decode_steps(eg, kind):
+    """Relative to the largest value: the weights' and the result's rounding, H each."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_step.py")
+    spec = importlib.util.spec_from_file_location("attention_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, bad, lens = mod.run(3, kind, verbose=False)
+    assert bad == 0 and lens == [p + 3 for p in mod.PROMPTS]
+    assert worst <= 4 * H
+
+
 def test_empty_inputs(eg):
     z = lambda *shape, dtype=torch.int16: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
     cache = eg.KVCache(eg.ENGRAM_CACHE_BF16, z(1, 1, 8, 32), z(1, 1, 8, 32))
