@@ -867,6 +867,8 @@ engram_status engram_project_mxfp4(const uint16_t *x, const uint8_t *codes, cons
               "x of %d x %d values exceeds %lld bytes", T, K,
               (long long)ENGRAM_MX_MAX_WEIGHT_BYTES);
   if (T == 0) return ENGRAM_OK;
+  REQUIRE_SUP(engram::project_fp4_blocks(T, N) <= kMaxBlocks / 2,
+              "%d tokens of %d columns are too many for one call", T, N);
   REQUIRE(x && codes && out && aligned(x, 16) && aligned(codes, 16) && aligned(out, 16),
           "x, codes or out is NULL or not 16-byte aligned");
   REQUIRE(scales, "scales is NULL");

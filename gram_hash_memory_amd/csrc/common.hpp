@@ -203,6 +203,7 @@ hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream);
 
 hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,
                                uint8_t *scales, hipStream_t stream);
+int64_t project_fp4_blocks(int32_t T, int32_t N);       // workgroups of 512 threads
 hipError_t launch_project_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
                               uint16_t *out, int32_t T, int32_t K, int32_t N, hipStream_t stream);
 

