@@ -4,9 +4,9 @@
 //   m = max_p scale q.k_p,  lse = m + log sum_p e^(scale q.k_p - m)
 //
 // Bound by reading the seen keys and values once: 64 ragged streams of up to
-// 4096 places in 8 bits, 333 MB, take 68 us (4.9 TB/s) and 5 us to join; one of
+// 4096 places in 8 bits, 333 MB, take 67 us (5.0 TB/s) and 5 us to join; one of
 // 131072 places in bf16, 537 MB, 93 us (5.8 TB/s) and 5.  One of 500 places takes
-// 9.6 us, by latency alone.  The query heads of one key-value head share a
+// 9.1 us, by latency alone.  The query heads of one key-value head share a
 // workgroup (up to 32 of them), so that each key and value is read once.  The
 // work of all sequences is cut into equal runs, a workgroup each (chunks of the
 // longest length instead: 76 to 92 us for the 64 streams); what of a run is not
@@ -65,6 +65,8 @@ constexpr int64_t kBlocks = 256;
 inline int64_t direct_units(int64_t pairs, int64_t unit_bytes) {
   return pairs < kBlocks ? 4 : std::max<int64_t>(4, std::min<int64_t>(16, 544 * 1024 / unit_bytes));
 }
+
+constexpr unsigned kResultLds = 49152;     // for the waves' results: 64 KB with the rest
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
   __shared__ int64_t page_lds[2][kMaxChunk / kMinPage + 1];   // a page's first row, or -1
   __shared__ int bad_lds[2][kW];
   __shared__ float2 ml_lds[2][kW][kHt][16];
-  extern __shared__ f32x4 o_lds[];           // [1 or 2][kW - 1][kAcc][4][heads of a tile]
+  extern __shared__ f32x4 o_lds[];           // [1 or 2][kW][kAcc][4][heads of a tile]
 
   const CacheView &c = a.cache;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -427,15 +429,16 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
   };
   reset();
 
-  // A piece's parts, the waves' results, to LDS; then joined by wave 0, in wave order.
+  // A piece's parts, the waves' results, to LDS; then joined by all threads, two
+  // neighbouring dimensions of four places in O^T each, in wave order.
   auto part_lds = [&](const Work &w) {
-    return o_lds + (sp.two_buffers ? (w.index & 1) * (kW - 1) * kAcc * 4 * min(16, heads_of(w)) : 0);
+    return o_lds + (sp.two_buffers ? (w.index & 1) * kW * kAcc * 4 * min(16, heads_of(w)) : 0);
   };
   auto give = [&](const Work &w, int t, int here) {
-    f32x4 *const ob = part_lds(w);
-    if (wave > 0 && col < here) {
+    f32x4 *const ob = part_lds(w) + wave * kAcc * 4 * here;
+    if (col < here) {
 #pragma unroll
-      for (int n = 0; n < kAcc; ++n) ob[((wave - 1) * kAcc + n) * 4 * here + g * here + col] = o[t][n];
+      for (int n = 0; n < kAcc; ++n) ob[n * 4 * here + g * here + col] = o[t][n];
     }
   };
   auto join = [&](const Work &w) {
@@ -450,49 +453,47 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
         give(w, t, here);
         barrier();
       }
-      if (wave > 0 || col >= here) continue;
-      float top = m[t];
+      for (int k = threadIdx.x; k < kAcc / 2 * 4 * here; k += 64 * kW) {
+        const int n = k / (4 * here) * 2, lane_of = k - n * 2 * here;      // (g, column) of the parts
+        const int gg = lane_of / here, head = lane_of - gg * here;
+        float top = -INFINITY, sum = 0.0f;
+        float2 ml[kW];
+        f32x4 part0[kW], part1[kW];
 #pragma unroll
-      for (int x = 1; x < kW; ++x) top = fmaxf(top, ml_lds[w.index & 1][x][t][col].x);
-      const float ms = top == -INFINITY ? 0.0f : top;
-      float keep = __builtin_amdgcn_exp2f(m[t] - ms), sum = l[t] * keep;
+        for (int x = 0; x < kW; ++x) {
+          ml[x] = ml_lds[w.index & 1][x][t][head];
+          part0[x] = ob[(x * kAcc + n) * 4 * here + lane_of];
+          part1[x] = ob[(x * kAcc + n + 1) * 4 * here + lane_of];
+          top = fmaxf(top, ml[x].x);
+        }
+        const float ms = top == -INFINITY ? 0.0f : top;
+        f32x4 a0{}, a1{};
 #pragma unroll
-      for (int n = 0; n < kAcc; ++n) o[t][n] *= keep;
-#pragma unroll 1
-      for (int x = 1; x < kW; ++x) {
-        const float2 ml = ml_lds[w.index & 1][x][t][col];
-        keep = __builtin_amdgcn_exp2f(ml.x - ms);
-        sum += ml.y * keep;
-#pragma unroll
-        for (int n = 0; n < kAcc; ++n)
-          o[t][n] += ob[((x - 1) * kAcc + n) * 4 * here + g * here + col] * keep;
-      }
-      const int64_t row = row0_of(w) + 16 * t + col;
-      // A run's first piece, or a later one (the run's last) that it does not hold whole.
-      const int64_t part = (2 * int64_t(blockIdx.x) + (w.index > 0)) * sp.block_heads + 16 * t + col;
-      const float inv = !w.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-      if (g == 0) {
-        if (!w.whole) sp.ml[part] = float2{top, sum};
-        else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-      }
-      each_piece<P::kN>([&](auto piece) {
-        constexpr int wd = P::width(piece.value), first = P::base(piece.value);
+        for (int x = 0; x < kW; ++x) {
+          const float keep = __builtin_amdgcn_exp2f(ml[x].x - ms);
+          sum += ml[x].y * keep;
+          a0 += part0[x] * keep;
+          a1 += part1[x] * keep;
+        }
+        const int64_t row = row0_of(w) + 16 * t + head;
+        // A run's first piece, or a later one (the run's last) that it does not hold whole.
+        const int64_t part = (2 * int64_t(blockIdx.x) + (w.index > 0)) * sp.block_heads + 16 * t + head;
+        const float inv = !w.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (k < here) {
+          if (!w.whole) sp.ml[part] = float2{top, sum};
+          else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+        int first = 0, wd = P::width(0);
+        each_piece<P::kN>([&](auto piece) {
+          if (16 * n >= P::base(piece.value)) first = P::base(piece.value), wd = P::width(piece.value);
+        });
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int d = first + wd * (4 * g + r);
-          if (w.whole) {
-            uint16_t *dst = a.out + row * D + d;
-#pragma unroll
-            for (int i = 0; i < wd / 2; ++i)
-              reinterpret_cast<uint32_t *>(dst)[i] = pack_bf16x2(
-                  o[t][first / 16 + 2 * i][r] * inv, o[t][first / 16 + 2 * i + 1][r] * inv);
-          } else {
-            float *dst = sp.o + part * D + d;
-#pragma unroll
-            for (int i = 0; i < wd; ++i) dst[i] = o[t][first / 16 + i][r];
-          }
+          const int d = first + wd * (4 * gg + r) + n - first / 16;
+          if (w.whole) *reinterpret_cast<uint32_t *>(a.out + row * D + d) = pack_bf16x2(a0[r] * inv, a1[r] * inv);
+          else *reinterpret_cast<float2 *>(sp.o + part * D + d) = float2{a0[r], a1[r]};
         }
-      });
+      }
     }
     reset();
     if (!sp.two_buffers) barrier();
@@ -728,22 +729,29 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Sp
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
-template <int kDb, bool kMx>
-void by_heads(const PagedAttention &a, Split sp, hipStream_t stream) {
-  unsigned lds = unsigned((kW - 1) * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
-  sp.two_buffers = 2 * lds <= 49152;             // 64 KB with the rest
+template <int kDb, bool kMx, int kHt>
+hipError_t launch(const PagedAttention &a, Split sp, hipStream_t stream) {
+  const void *kernel = reinterpret_cast<const void *>(&paged_attention_kernel<kDb, kMx, kHt>);
+  unsigned lds = unsigned(kW * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
+  sp.two_buffers = 2 * lds <= kResultLds;
   if (sp.two_buffers) lds *= 2;
-  const dim3 grid(sp.blocks), block(64 * kW);
-  if (sp.block_heads > 16)
-    hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, 2>), grid, block, lds, stream, a, sp);
-  else
-    hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, 1>), grid, block, lds, stream, a, sp);
+  if (lds > kResultLds) {                    // more than a launch may have without asking
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((paged_attention_kernel<kDb, kMx, kHt>), dim3(sp.blocks), dim3(64 * kW),
+                     lds, stream, a, sp);
+  return hipGetLastError();
+}
+
+template <int kDb, bool kMx>
+hipError_t by_heads(const PagedAttention &a, const Split &sp, hipStream_t stream) {
+  return sp.block_heads > 16 ? launch<kDb, kMx, 2>(a, sp, stream) : launch<kDb, kMx, 1>(a, sp, stream);
 }
 
 template <int kDb>
-void by_format(const PagedAttention &a, const Split &sp, hipStream_t stream) {
-  if (a.cache.k_scales) by_heads<kDb, true>(a, sp, stream);
-  else by_heads<kDb, false>(a, sp, stream);
+hipError_t by_format(const PagedAttention &a, const Split &sp, hipStream_t stream) {
+  return a.cache.k_scales ? by_heads<kDb, true>(a, sp, stream) : by_heads<kDb, false>(a, sp, stream);
 }
 
 inline int block_heads(int q_heads, int kv_heads) { return std::min(kHeadBlock, q_heads / kv_heads); }
@@ -780,17 +788,17 @@ hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream) {
     sp.ml = reinterpret_cast<float2 *>(sp.o + parts * D);
     sp.before = reinterpret_cast<int32_t *>(sp.ml + parts);
   }
+  hipError_t err;
   switch (D / 32) {
-    case 1: by_format<1>(a, sp, stream); break;
-    case 2: by_format<2>(a, sp, stream); break;
-    case 3: by_format<3>(a, sp, stream); break;
-    case 4: by_format<4>(a, sp, stream); break;
-    case 5: by_format<5>(a, sp, stream); break;
-    case 6: by_format<6>(a, sp, stream); break;
-    case 7: by_format<7>(a, sp, stream); break;
-    default: by_format<8>(a, sp, stream);
+    case 1: err = by_format<1>(a, sp, stream); break;
+    case 2: err = by_format<2>(a, sp, stream); break;
+    case 3: err = by_format<3>(a, sp, stream); break;
+    case 4: err = by_format<4>(a, sp, stream); break;
+    case 5: err = by_format<5>(a, sp, stream); break;
+    case 6: err = by_format<6>(a, sp, stream); break;
+    case 7: err = by_format<7>(a, sp, stream); break;
+    default: err = by_format<8>(a, sp, stream);
   }
-  const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.direct) return err;
   hipLaunchKernelGGL(join_kernel, dim3(unsigned(int64_t(a.n_seqs) * a.q_heads)),
                      dim3(kJoinThreads), 0, stream, a, sp);
