@@ -473,30 +473,30 @@ class KVCache:
 
 
 def _strided(t, dtype, dims: int, name: str):
-    """Device pointer of a GPU tensor whose last dimension is contiguous."""
+    """Device pointer and strides of a GPU tensor whose last dimension is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    strides = t.stride()
+    if len(strides) != dims or (strides[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), strides
 
 
 def engram_cache_write(cache: KVCache, k, v, slots, bad_slots=None, stream=None) -> None:
     """Keys and values int16 [T, kv_heads, head_dim] (bf16 bits; views with token and head
     strides of multiples of 8) into the cache's places slots int64 [T]."""
-    T = int(k.shape[0])
-    want = (T, cache.kv_heads, cache.head_dim)
-    if tuple(k.shape) != want or tuple(v.shape) != want:
+    T, heads = int(k.shape[0]), cache.kv_heads
+    want = (T, heads, cache.head_dim)
+    if k.shape != want or v.shape != want:
         raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
-
-    def strides(x):      # a dimension of size 1 has no stride of its own; torch may report any
-        return (x.stride(0) if T > 1 else 0,
-                x.stride(1) if cache.kv_heads > 1 else cache.head_dim)
+    pk, sk = _strided(k, torch.int16, 3, "k")
+    pv, sv = _strided(v, torch.int16, 3, "v")
+    if T <= 1 or heads <= 1:     # a dimension of size 1 has no stride of its own; torch may report any
+        sk, sv = ((x[0] if T > 1 else 0, x[1] if heads > 1 else cache.head_dim) for x in (sk, sv))
     _check(_lib.engram_cache_write(
-        cache.address, _strided(k, torch.int16, 3, "k"), *strides(k),
-        _strided(v, torch.int16, 3, "v"), *strides(v),
+        cache.address, pk, sk[0], sk[1], pv, sv[0], sv[1],
         _dptr(slots, torch.int64, T, "slots"), T, _dptr(bad_slots, torch.int32, 1, "bad_slots"),
         _stream(stream)))
 
@@ -519,14 +519,14 @@ def engram_qk_norm_rope(qkv, q_heads: int, kv_heads: int, head_dim: int, q_weigh
     (a view with a row stride of a multiple of 8 will do): queries to q [T, q_heads,
     head_dim], keys to k [T, kv_heads, head_dim] and / or, with the row's values, into the
     cache's places slots int64 [T].  positions int32 [T], inv_freq float64 [rotary_dim / 2]."""
-    p = _strided(qkv, torch.int16, 2, "qkv")
+    p, strides = _strided(qkv, torch.int16, 2, "qkv")
     T, width = qkv.shape
     need = (q_heads + (kv_heads if cache is None else 2 * kv_heads)) * head_dim
     if width < need:
         raise ValueError(f"qkv has rows of {width} values, needs {need}")
     # A single row has no stride of its own; torch may report any.
     _check(_lib.engram_qk_norm_rope(
-        p, qkv.stride(0) if T > 1 else (need + 7) // 8 * 8, T, q_heads, kv_heads, head_dim,
+        p, strides[0] if T > 1 else (need + 7) // 8 * 8, T, q_heads, kv_heads, head_dim,
         _dptr(q_weight, torch.int16, head_dim, "q_weight"),
         _dptr(k_weight, torch.int16, head_dim, "k_weight"), eps,
         _dptr(positions, torch.int32, T, "positions"),
@@ -548,12 +548,13 @@ def engram_paged_attention(cache: KVCache, q, table, lens, max_len: int, scale: 
                            stream=None) -> None:
     """Attention of one new token per sequence: q, out int16 [n_seqs, q_heads, head_dim],
     table int32 [n_seqs, pages], lens int32 [n_seqs], lse float32 [n_seqs, q_heads]."""
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be [n_seqs, q_heads, {cache.head_dim}], got {tuple(q.shape)}")
-    if table.dim() != 2 or table.shape[0] != q.shape[0]:
-        raise ValueError(f"table must be [n_seqs={q.shape[0]}, pages], got {tuple(table.shape)}")
-    n, heads, D = q.shape
-    width = int(table.shape[1])
+    shape, pages = q.shape, table.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [n_seqs, q_heads, {cache.head_dim}], got {tuple(shape)}")
+    if len(pages) != 2 or pages[0] != shape[0]:
+        raise ValueError(f"table must be [n_seqs={shape[0]}, pages], got {tuple(pages)}")
+    n, heads, D = shape
+    width = pages[1]
     _check(_lib.engram_paged_attention(
         cache.address, _dptr(q, torch.int16, 0, "q"), _dptr(table, torch.int32, 0, "table"),
         width, _dptr(lens, torch.int32, n, "lens"), n, heads, max_len, scale, window,
