@@ -14,10 +14,11 @@
 // so its 8 angles serve every head.
 //
 // Waves have queries only, in fp32, or keys too, in fp64: a cache in 8 bits
-// rounds the keys again, and fp32 leaves 3 values of 2048 x 8 x 128 on the wrong side
-// of both borders at once, a whole step of 8 bits off (fp64 none).  At 8192 tokens that costs 1.7 us.  Two passes a wave and 5
-// waves a SIMD: one register more for each value in flight costs more than it
-// brings (4 passes, 117 registers: 36.4 us).
+// rounds the keys again, and fp32 leaves 3 values of 2048 x 8 x 128 on the wrong
+// side of both borders at once, a whole step of 8 bits off (fp64 none).  At 8192
+// tokens that costs 1.7 us.  Two passes a wave and 5 waves a SIMD: one register
+// more for each value in flight costs more than it brings (4 passes, 117
+// registers: 36.4 us).
 #include "kv_cache.hpp"
 
 namespace engram {
@@ -44,7 +45,7 @@ __device__ __forceinline__ void unpack8(const u32x4 q, float *x) {
 }
 
 // cos(pi t), sin(pi t) for |t| <= 1: the quarter turn it is in, and the series
-// of the rest, at most pi/4 away (the first terms left out are below 2^-45).
+// of the rest, at most pi/4 away (the first terms left out are below 2^-41).
 __device__ __forceinline__ double2 cos_sin(double t) {
   const double quarter = rint(2.0 * t), x = (t - 0.5 * quarter) * 3.14159265358979323846;
   const double y = x * x;
