@@ -582,7 +582,7 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
               held.v[j][i] = shown >> j & 1 ? held.v[j][i] : 0;
         }
 
-        bf16x8 wt[kHt];                             // the weights, as B operands
+        bf16x8 wt[kHt], wt_rest[kHt];               // the weights, as B operands
 #pragma unroll
         for (int t = 0; t < kHt; ++t) {
           float e[8];
@@ -612,9 +612,19 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
             sum += e[j];
           }
           l[t] += sum;
-          // Rounded to bf16 for the matrix cores; the sum is of the fp32 ones.
-          wt[t] = as_frag(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                         pack_bf16x2(e[6], e[7]));
+          // For the matrix cores each is the sum of two bf16 values: its upper 16 bits,
+          // and what they leave, below 2^-7 of it, rounded: 2^-15 off.  The sum is of
+          // the fp32 ones.
+          uint32_t top16[4], rest[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a = __float_as_uint(e[2 * j]), b = __float_as_uint(e[2 * j + 1]);
+            top16[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            rest[j] = pack_bf16x2(e[2 * j] - __uint_as_float(a & 0xFFFF0000u),
+                                  e[2 * j + 1] - __uint_as_float(b & 0xFFFF0000u));
+          }
+          wt[t] = as_frag(top16[0], top16[1], top16[2], top16[3]);
+          wt_rest[t] = as_frag(rest[0], rest[1], rest[2], rest[3]);
         }
 
         each_piece<P::kN>([&](auto piece) {
@@ -643,6 +653,8 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
             for (int t = 0; t < kHt; ++t) {
               o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, wt[t], o[t][n], 0, 0, 0);
               o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, wt[t], o[t][n + 1], 0, 0, 0);
+              o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, wt_rest[t], o[t][n], 0, 0, 0);
+              o[t][n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, wt_rest[t], o[t][n + 1], 0, 0, 0);
             }
           }
         });

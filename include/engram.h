@@ -575,8 +575,8 @@ ENGRAM_API size_t engram_paged_attention_workspace_bytes(int32_t n_seqs, int32_t
  *     out = sum_p exp(scale q.k_p) v_p / sum_p exp(scale q.k_p), in bf16;
  *     lse (DEVICE fp32 [n_seqs][q_heads], nullable) = log sum_p exp(scale q.k_p).
  *   Where nothing is seen out is 0 and lse -infinity.  Scores, softmax
- *   statistics and sums are held in fp32; the weights exp(.) are rounded to
- *   bf16 for the matrix cores, and their sum is that of the fp32 ones.
+ *   statistics and sums are held in fp32; for the matrix cores each weight
+ *   exp(.) is the sum of two bf16 values, at most 2^-15 of it off.
  *   Sequences are split over their length where there are too few of them to
  *   fill the GPU; the parts are joined in a fixed order, so results do not
  *   depend on timing.

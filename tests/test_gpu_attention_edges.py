@@ -1,0 +1,65 @@
+"""The attention step's operators where a rounding, an infinity or the split of the work could show, on the GPU.
+
+Against oracle/attention.py (float64), with the bounds of tests/test_gpu_attention.py (u = 2^-24 of fp32, h = 2^-8
+the half step of bf16) but for the softmax's weights: held as the sum of two bf16 values, of which the second has at
+most 2^-7 of the whole, they are off by 2^-7 h = 2^-15.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from oracle import attention as oa
+from test_gpu_attention import H, U, Guarded, bits, dev, eg, host, make_cache, within  # noqa: F401 (eg: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+class Call:
+    """One call of the attention: a cache of unrelated pages, lengths, queries; its outputs checked on request."""
+
+    def __init__(self, eg, rng, fmt, ps, hq, hkv, D, lens, window=0, sharp=2.0, width=None):
+        lens = np.asarray(lens, np.int32)
+        n, self.max_len = len(lens), int(lens.max())
+        width = max(1, -(-self.max_len // ps))
+        need = -(-lens // ps)
+        self.arrays, self.held, self.cache = make_cache(eg, rng, fmt, int(need.sum()) + 1, hkv, ps, D)
+        perm = rng.permutation(int(need.sum()) + 1)
+        table = np.full((n, width), -1, np.int32)
+        table[np.arange(width) < need[:, None]] = perm[:need.sum()]
+        self.q, self.table, self.lens, self.window, self.scale = bits(sharp * rng.normal(size=(n, hq, D))), table, lens, window, D ** -0.5
+        self.on_gpu = [dev(a) for a in (self.q, table, lens)]
+        self.out, self.lse = (n, hq, D), (n, hq)
+        self.bytes = eg.engram_paged_attention_workspace_bytes(n, hq, hkv, D, self.max_len)
+        self.eg = eg
+
+    def run(self):
+        import torch
+        out, lse = Guarded(self.out, torch.int16), Guarded(self.lse, torch.float32)
+        ws, bad = Guarded((self.bytes,), torch.uint8), torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.eg.engram_paged_attention(self.cache, *self.on_gpu, self.max_len, self.scale, out.t, ws.t,
+                                       window=self.window, lse=lse.t, bad_pages=bad)
+        ws.host()
+        assert bad.item() == 0
+        return out.host(), lse.host()
+
+    def check(self, out, lse):
+        D = self.q.shape[2]
+        want, want_lse, spread, logit = oa.paged_attention(*self.arrays, self.q, self.table, self.lens, self.max_len,
+                                                           self.scale, self.window)
+        d = D * U * logit
+        within(out, want, H * np.abs(want) + (2.0 ** -15 + 2 * d + 2.0 ** -18)[..., None] * spread + 1e-30)
+        empty = np.isneginf(want_lse)
+        assert np.array_equal(empty, np.isneginf(lse)) and not out[empty].any()
+        got, ref = lse[~empty].astype(np.float64), want_lse[~empty]
+        tol = d[~empty] + (self.max_len / 32 + 32) * U + 4 * U * np.abs(ref)
+        assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) / tol)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("hq,hkv,D,lens", [(8, 2, 32, [500, 130, 1]), (20, 1, 32, [700, 33]), (3, 1, 96, [3000]),
+                                           (32, 8, 128, [400, 129]), (32, 1, 256, [200, 1500])])
+def test_paged_attention_weights_are_not_rounded_to_bf16(eg, fmt, hq, hkv, D, lens):
+    """Nearly equal weights over many values: results small against the values, so that weights in 8 bits would show."""
+    call = Call(eg, np.random.default_rng(D + hq), fmt, 16, hq, hkv, D, lens, sharp=0.1)
+    call.check(*call.run())
