@@ -29,19 +29,19 @@
 // first places are requested before this one's results are joined in LDS.
 #include <algorithm>
 
+#include "attention_lds.hpp"
 #include "kv_cache.hpp"
 
 namespace engram {
 namespace {
 
-using kvc::row_index;
+using attn::kHeadBlock;
+using attn::kW;
 
 constexpr int kTile = 32;                  // places a wave takes at a time
-constexpr int kW = 4;                      // waves of a workgroup
 constexpr int kUnit = kTile * kW;          // places the work is dealt out by
 constexpr int kMaxChunk = 4096;            // places whose pages are held in LDS at a time
 constexpr int kMinPage = 8;
-constexpr int kHeadBlock = 32;             // query heads of a workgroup
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- the plan
@@ -65,8 +65,6 @@ constexpr int64_t kBlocks = 256;
 inline int64_t direct_units(int64_t pairs, int64_t unit_bytes) {
   return pairs < kBlocks ? 4 : std::max<int64_t>(4, std::min<int64_t>(16, 544 * 1024 / unit_bytes));
 }
-
-constexpr unsigned kResultLds = 49152;     // for the waves' results: 64 KB with the rest
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -95,7 +93,7 @@ struct Split {
   float2 *ml;
   int32_t *before;         // [n_seqs + 1], [n_seqs + 1] units of a run
   int32_t blocks, head_blocks, block_heads;
-  bool direct, two_buffers;  // the latter: of LDS for the waves' results
+  bool direct;
 };
 
 // How the head_dim = 32 * kDb dimensions fall to 16 lanes: pieces of 16, 8, 4,
@@ -432,7 +430,7 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
   // A piece's parts, the waves' results, to LDS; then joined by all threads, two
   // neighbouring dimensions of four places in O^T each, in wave order.
   auto part_lds = [&](const Work &w) {
-    return o_lds + (sp.two_buffers ? (w.index & 1) * kW * kAcc * 4 * min(16, heads_of(w)) : 0);
+    return o_lds + attn::part_begin(kAcc, sp.block_heads, w.index);
   };
   auto give = [&](const Work &w, int t, int here) {
     f32x4 *const ob = part_lds(w) + wave * kAcc * 4 * here;
@@ -496,7 +494,7 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
       }
     }
     reset();
-    if (!sp.two_buffers) barrier();
+    if (!attn::two_buffers(kAcc, sp.block_heads)) barrier();
   };
 
   Work w{};
@@ -742,12 +740,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(PagedAttention a, Sp
 }
 
 template <int kDb, bool kMx, int kHt>
-hipError_t launch(const PagedAttention &a, Split sp, hipStream_t stream) {
+hipError_t launch(const PagedAttention &a, const Split &sp, hipStream_t stream) {
   const void *kernel = reinterpret_cast<const void *>(&paged_attention_kernel<kDb, kMx, kHt>);
-  unsigned lds = unsigned(kW * (2 * kDb) * 4 * std::min(16, sp.block_heads) * sizeof(f32x4));
-  sp.two_buffers = 2 * lds <= kResultLds;
-  if (sp.two_buffers) lds *= 2;
-  if (lds > kResultLds) {                    // more than a launch may have without asking
+  const unsigned lds = attn::result_bytes(2 * kDb, sp.block_heads);
+  if (lds > attn::kResultLds) {              // more than a launch may have without asking
     const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }

@@ -63,3 +63,30 @@ def test_paged_attention_weights_are_not_rounded_to_bf16(eg, fmt, hq, hkv, D, le
     """Nearly equal weights over many values: results small against the values, so that weights in 8 bits would show."""
     call = Call(eg, np.random.default_rng(D + hq), fmt, 16, hq, hkv, D, lens, sharp=0.1)
     call.check(*call.run())
+
+
+def run_pieces(call, hkv, head_blocks):
+    """Whole or partial (sequence, heads) pairs of each of the 256 runs, as the call deals them out."""
+    units = np.repeat(-(-call.lens // 128), hkv * head_blocks)
+    per = max(1, -(-int(units.sum()) // 256))
+    ends = np.cumsum(units)
+    held = units > 0
+    first, last = (ends - units)[held] // per, (ends - 1)[held] // per
+    return np.bincount(np.concatenate([np.arange(a, b + 1) for a, b in zip(first, last)]))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("hq,hkv,D", [(70, 1, 64), (71, 1, 32), (40, 1, 96), (66, 2, 64), (64, 1, 64), (47, 1, 96)])
+def test_paged_attention_runs_of_blocks_of_differing_heads(eg, fmt, hq, hkv, D):
+    """Runs of many pieces whose blocks have 32 query heads, then a few: pieces shorter than a workgroup's four
+    tiles beside long ones.  The same bits every time."""
+    rng = np.random.default_rng(hq + D)
+    lens = np.concatenate([rng.integers(1, 128, size=25), rng.integers(0, 32, size=15), rng.integers(900, 2000, size=20)])
+    call = Call(eg, rng, fmt, 16, hq, hkv, D, rng.permutation(lens))
+    blocks = -(-hq // hkv // 32)
+    assert call.bytes > 0 and run_pieces(call, hkv, blocks).max() > 2
+    out, lse = call.run()
+    call.check(out, lse)
+    for _ in range(4):
+        again = call.run()
+        assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
