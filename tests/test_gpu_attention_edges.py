@@ -10,7 +10,7 @@ import pytest
 
 import oracle
 from oracle import attention as oa
-from test_gpu_attention import H, U, Guarded, bits, dev, eg, host, make_cache, within  # noqa: F401 (eg: the fixture)
+from test_gpu_attention import H, U, Guarded, bits, dev, eg, make_cache, within  # noqa: F401 (eg: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,21 @@ def test_paged_attention_runs_of_blocks_of_differing_heads(eg, fmt, hq, hkv, D):
     for _ in range(4):
         again = call.run()
         assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt,hq,hkv,D,n,top", [("mxfp8", 3, 1, 32, 700, 2300), ("bf16", 4, 2, 64, 300, 2100),
+                                                ("mxfp8", 2, 2, 32, 513, 2500)])
+def test_paged_attention_many_sequences_dealt_out_in_runs(eg, fmt, hq, hkv, D, n, top):
+    """More sequences than a workgroup has threads, split over their length: several of them a thread's, empty ones
+    at the ends of its span and whole spans of them among them."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, top // 2, size=n)
+    lens[rng.random(n) < 0.2] = 0
+    per_thread = -(-n // 256)
+    lens[:per_thread] = 0                                     # the first thread's
+    lens[5 * per_thread - 1:5 * per_thread + 1] = 0           # one thread's last, another's first
+    lens[20 * per_thread:21 * per_thread] = 0
+    lens[[-1, n // 2]] = [0, top]
+    call = Call(eg, rng, fmt, 8, hq, hkv, D, lens)
+    assert call.bytes > 0
+    call.check(*call.run())
