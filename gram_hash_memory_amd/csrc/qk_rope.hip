@@ -95,10 +95,10 @@ __global__ __launch_bounds__(kThreads, 5) void qk_norm_rope_kernel(QkRope a) {
   const int part = int(id - t * a.waves_per_token);
   // Passes of queries only, and the others: waves of their own.
   const int q_passes = a.q_heads / kRows, kv_passes = (a.heads + kRows - 1) / kRows - q_passes;
-  const int kv_waves = a.waves_per_token - a.q_waves, kv_part = part - a.q_waves;
+  const int kv_part = part - a.q_waves;
   const bool keys = kv_part >= 0;
-  const int pass0 = keys ? q_passes + kv_passes * kv_part / kv_waves : q_passes * part / a.q_waves;
-  const int pass1 = keys ? q_passes + kv_passes * (kv_part + 1) / kv_waves : q_passes * (part + 1) / a.q_waves;
+  const int pass0 = keys ? q_passes + kPass * kv_part : kPass * part;
+  const int pass1 = min(pass0 + kPass, keys ? q_passes + kv_passes : q_passes);
   const int D = a.head_dim, half = a.rotary_dim / 2;
 
   // All of the wave's rows are requested before anything is waited for.

@@ -10,7 +10,7 @@ import pytest
 
 import oracle
 from oracle import attention as oa
-from test_gpu_attention import H, U, Guarded, bits, dev, eg, make_cache, within  # noqa: F401 (eg: a fixture)
+from test_gpu_attention import H, U, Guarded, bits, dev, eg, make_cache, rope_inputs, within  # noqa: F401 (eg: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,20 @@ def test_paged_attention_many_sequences_dealt_out_in_runs(eg, fmt, hq, hkv, D, n
     call = Call(eg, rng, fmt, 8, hq, hkv, D, lens)
     assert call.bytes > 0
     call.check(*call.run())
+
+
+# ---------------------------------------------------------------- norm and rotation
+
+@pytest.mark.parametrize("hq,hkv", [((1 << 20) + 650, 2), (33, (1 << 20) + 650)])
+def test_qk_norm_rope_of_a_million_heads(eg, hq, hkv):
+    """A row whose passes times its waves pass 32 bits."""
+    import torch
+    T, D = 1, 32
+    row, qkv, qw, kw, pos, inv = rope_inputs(np.random.default_rng(hkv), T, hq, hkv, D, D, 0, 5000)
+    q, k = Guarded((T, hq, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    eg.engram_qk_norm_rope(qkv, hq, hkv, D, dev(qw), dev(kw), 1e-6, dev(pos), dev(inv), False, q.t, k.t)
+    x = row.reshape(T, -1, D)
+    for got, first, n, w in ((q.host(), 0, hq, qw), (k.host(), hq, hkv, kw)):
+        for h in range(0, n, 1 << 18):
+            want, mag = oa.qk_norm_rope(x[:, first + h:first + min(n, h + (1 << 18))], w, 1e-6, pos, inv, False)
+            within(got[:, h:h + (1 << 18)], want, H * np.abs(want) + 2.0 ** -20 * mag + 1e-38)
