@@ -226,10 +226,10 @@ __global__ __launch_bounds__(kThreads, 5) void qk_norm_rope_kernel(QkRope a) {
       for (int j = 0; j < 8; ++j) {
         const int ia = kInter ? 2 * j : j, ib = kInter ? 2 * j + 1 : 8 + j;
         const double2 v = cs[my_cs + j];
-        const double c = rotated ? v.x : 1.0, sn = rotated ? v.y : 0.0;
         const double p = double(x[ia] * w[ia]), q = double(x[ib] * w[ib]);
-        x[ia] = float(fma(p, c, -(q * sn)) * r);
-        x[ib] = float(fma(q, c, p * sn) * r);
+        // (Not a rotation by 0 past rotary_dim: an infinity times 0 is NaN.)
+        x[ia] = float((rotated ? fma(p, v.x, -(q * v.y)) : p) * r);
+        x[ib] = float((rotated ? fma(q, v.x, p * v.y) : q) * r);
       }
       if (!is_v) ra[i] = pack8(x, 1.0f), rb[i] = pack8(x + 8, 1.0f);
     }

@@ -125,3 +125,26 @@ def test_qk_norm_rope_of_a_million_heads(eg, hq, hkv):
         for h in range(0, n, 1 << 18):
             want, mag = oa.qk_norm_rope(x[:, first + h:first + min(n, h + (1 << 18))], w, 1e-6, pos, inv, False)
             within(got[:, h:h + (1 << 18)], want, H * np.abs(want) + 2.0 ** -20 * mag + 1e-38)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (32, 8)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_qk_norm_rope_infinity_spoils_its_own_pair_only(eg, hq, hkv, inter):
+    """An infinity makes its head's mean infinite and all finite values 0: NaN is left of it, and of its partner
+    where it is rotated."""
+    import torch
+    rng = np.random.default_rng(3)
+    T, D, rot = 4, 64, 32
+    row, qkv, qw, kw, pos, inv = rope_inputs(rng, T, hq, hkv, D, rot, 0, 1000)
+    x = row.reshape(T, -1, D)
+    for t, d in ((0, 40), (1, 63), (2, 5), (3, 32)):
+        x[t, :, d] = 0x7F80 if t % 2 else 0xFF80
+    qkv = dev(row)
+    q, k = Guarded((T, hq, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    eg.engram_qk_norm_rope(qkv, hq, hkv, D, dev(qw), dev(kw), 1e-6, dev(pos), dev(inv), inter, q.t, k.t)
+    for got, xs, w in ((q, x[:, :hq], qw), (k, x[:, hq:hq + hkv], kw)):
+        with np.errstate(invalid="ignore"):
+            want, _ = oa.qk_norm_rope(xs, w, 1e-6, pos, inv, inter)
+        value = oracle.bf16_value(got.host())
+        assert np.array_equal(np.isnan(want), np.isnan(value))
+        assert not value[~np.isnan(want)].any() and not want[~np.isnan(want)].any()
