@@ -13,12 +13,16 @@
 // and 2 sub + 1.  In either layout its 8 pairs are the pairs 8 sub .. 8 sub + 7,
 // so its 8 angles serve every head.
 //
-// Waves have queries only, in fp32, or keys too, in fp64: a cache in 8 bits
-// rounds the keys again, and fp32 leaves 3 values of 2048 x 8 x 128 on the wrong
-// side of both borders at once, a whole step of 8 bits off (fp64 none).  At 8192
-// tokens that costs 1.7 us.  Two passes a wave and 5 waves a SIMD: one register
-// more for each value in flight costs more than it brings (4 passes, 117
-// registers: 36.4 us).
+// Waves have queries only, in fp32, or keys too (and the queries that share a
+// pass with them), in fp64: a cache in 8 bits rounds the keys again, and fp32
+// leaves 3 values of 2048 x 8 x 128 on the wrong side of both borders at once, a
+// whole step of 8 bits off (fp64 none).  At 8192 tokens that costs 1.7 us.  An
+// fp64 result is rounded to fp32 and that to bf16, as a conversion of a double
+// does: 1 in 2^17 is then half-way between two bf16 values and goes to the even
+// one (one rounding instead: 1 us more of 31 for 2048 tokens).
+//
+// Two passes a wave and 5 waves a SIMD: one register more for each value in
+// flight costs more than it brings (4 passes, 117 registers: 36.4 us).
 #include "kv_cache.hpp"
 
 namespace engram {
@@ -194,8 +198,8 @@ __global__ __launch_bounds__(kThreads, 5) void qk_norm_rope_kernel(QkRope a) {
     return;
   }
 
-  // With keys: in fp64 up to the rounding to bf16, so that what an 8-bit cache
-  // rounds again lies on the right side of its borders.
+  // With keys: in fp64 up to the results, so that what an 8-bit cache rounds again
+  // lies on the right side of its borders.
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     if (pass0 + i >= pass1) break;

@@ -148,3 +148,22 @@ def test_qk_norm_rope_infinity_spoils_its_own_pair_only(eg, hq, hkv, inter):
         value = oracle.bf16_value(got.host())
         assert np.array_equal(np.isnan(want), np.isnan(value))
         assert not value[~np.isnan(want)].any() and not want[~np.isnan(want)].any()
+
+
+def test_qk_norm_rope_keys_are_fp64_results_rounded_to_fp32_and_bf16(eg):
+    """Of 4 M keys, some 30 have an fp32 rounding half-way between two bf16 values: it goes to the even one."""
+    import torch
+    T, hq, hkv, D = 4096, 1, 8, 128
+    row, qkv, qw, kw, pos, inv = rope_inputs(np.random.default_rng(4), T, hq, hkv, D, D, 0, 4000)
+    q, k = Guarded((T, hq, D), torch.int16), Guarded((T, hkv, D), torch.int16)
+    eg.engram_qk_norm_rope(qkv, hq, hkv, D, dev(qw), dev(kw), 1e-6, dev(pos), dev(inv), False, q.t, k.t)
+    x = row.reshape(T, -1, D)[:, hq:hq + hkv]
+    want, mag = oa.qk_norm_rope(x, kw, 1e-6, pos, inv, False)
+    # The two fp64 computations are off by less than 2^-34 of their terms (angles of up to 4000 and a series
+    # to 2^-41): what is nearer to a border than that may go either way.
+    twice = [bits((want + e * mag).astype(np.float32)) for e in (-2.0 ** -34, 0.0, 2.0 ** -34)]
+    sure = (twice[0] == twice[2]) & (np.abs(want) > 1e-30)
+    assert sure.mean() > 0.999
+    assert (sure & (twice[1] != bits(want))).sum() > 10          # there are such
+    wrong = sure & (k.host() != twice[1])
+    assert not wrong.any(), int(wrong.sum())
