@@ -10,7 +10,8 @@ import pytest
 
 import oracle
 from oracle import attention as oa
-from test_gpu_attention import H, U, Guarded, bits, dev, eg, make_cache, rope_inputs, within  # noqa: F401 (eg: a fixture)
+from test_gpu_attention import (H, U, Guarded, bits, check_attention, dev, eg, host, make_cache,  # noqa: F401 (eg: a fixture)
+                                rope_inputs, step, step_state, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +168,17 @@ def test_qk_norm_rope_keys_are_fp64_results_rounded_to_fp32_and_bf16(eg):
     assert (sure & (twice[1] != bits(want))).sum() > 10          # there are such
     wrong = sure & (k.host() != twice[1])
     assert not wrong.any(), int(wrong.sum())
+
+
+# ---------------------------------------------------------------- the operators together
+
+def test_step_with_lse(eg):
+    """The decode step's attention with its own log-sum-exp."""
+    import torch
+    s = step_state(eg)
+    step(eg, s)
+    out, lse = Guarded(s["att"].shape, torch.int16), Guarded(s["att"].shape[:2], torch.float32)
+    eg.engram_paged_attention(s["cache"], s["q"], s["table"], s["lens"], 48, 0.125, out.t, s["ws"], lse=lse.t)
+    assert np.array_equal(out.host(), host(s["att"]))
+    check_attention(out.host(), lse.host(), [g.host() for g in s["held"]], host(s["q"]), host(s["table"]),
+                    host(s["lens"]), 48, 0.125, 0)
