@@ -614,6 +614,9 @@ ENGRAM_API engram_status engram_quantize_mxfp4(const uint16_t *w, int32_t N, int
  *   once.  Made for up to some 128 tokens, where reading the weight is what
  *   takes time; more tokens are right but run in tiles that each read it again.
  *   Limits: N * K/2 and T * K * 2 <= ENGRAM_MX_MAX_WEIGHT_BYTES.
+ *   engram_layer holds no 4-bit wkv.  A program that keeps one runs the stages:
+ *   engram_hash, engram_rows, this call (x = rows, K = cols * 256, N = (hc + 1)
+ *   * dim, out = kv), engram_gate.
  */
 ENGRAM_API engram_status engram_project_mxfp4(const uint16_t *x, const uint8_t *codes,
                                               const uint8_t *scales, uint16_t *out, int32_t T,

@@ -182,3 +182,34 @@ def test_step_with_lse(eg):
     assert np.array_equal(out.host(), host(s["att"]))
     check_attention(out.host(), lse.host(), [g.host() for g in s["held"]], host(s["q"]), host(s["table"]),
                     host(s["lens"]), 48, 0.125, 0)
+
+
+def test_engram_stages_with_a_4_bit_wkv(eg):
+    """Hash, rows, 4-bit projection and gate of the tiny workload: kv against the oracle's product of the same rows
+    and weight, and the highway what the gate makes of that kv."""
+    import torch
+
+    import workloads
+    from workloads.device import to_device
+    wl = workloads.make_workload(0)
+    sp, d = wl.spec, to_device(wl, "cuda")
+    layer = d.layers[0]
+    params, tokens = eg.HashParams.from_dict(wl.hash_params), eg.Tokens(d.cids, d.cu_seqlens)
+    codes, scales = Guarded((sp.N, sp.K // 2), torch.uint8), Guarded((sp.N, sp.K // 32), torch.uint8)
+    eg.engram_quantize_mxfp4(layer.wkv, sp.N, sp.K, codes.t, scales.t)
+    ids = torch.empty(sp.T, sp.cols, dtype=torch.int32, device="cuda")
+    rows, kv = Guarded((sp.T, sp.K), torch.int16), Guarded((sp.T, sp.N), torch.int16)
+    eg.engram_hash(params, tokens, ids)
+    eg.engram_rows(eg.ENGRAM_ROWS_Q2K, layer.table, None, sp.num_rows, ids, sp.cols, sp.cols, sp.T, rows.t)
+    eg.engram_project_mxfp4(rows.t, codes.t, scales.t, kv.t, sp.T, sp.K, sp.N)
+    h = d.h.clone()
+    eg.engram_gate(h, kv.t, layer.q_weight, layer.k_weight, None, sp.T, sp.hc, sp.dim, sp.eps, sp.clamp, sp.dot_scale)
+    want_codes, want_scales = oa.quantize_mxfp4(wl.layers[0].wkv)
+    assert np.array_equal(codes.host(), want_codes) and np.array_equal(scales.host(), want_scales)
+    want, mag = oa.project_mxfp4(rows.host(), want_codes, want_scales)
+    within(kv.host(), want, H * np.abs(want) + sp.K * U * mag)
+    want_h, a = oracle.gate(wl.h, kv.host(), wl.layers[0].q_weight, wl.layers[0].k_weight, None, sp.eps, sp.clamp,
+                            sp.dot_scale, return_preact=True)
+    # The bounds of the gate's own tests: 1e-2, and 1e-4 away from the steep part of its signed square root.
+    err = np.abs(h.cpu().numpy() - want_h) / np.maximum(1.0, np.abs(want_h))
+    assert err.max() <= 1e-2 and err[np.abs(a) > 1e-2].max() <= 1e-4
