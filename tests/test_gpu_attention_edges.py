@@ -213,3 +213,22 @@ def test_engram_stages_with_a_4_bit_wkv(eg):
     # The bounds of the gate's own tests: 1e-2, and 1e-4 away from the steep part of its signed square root.
     err = np.abs(h.cpu().numpy() - want_h) / np.maximum(1.0, np.abs(want_h))
     assert err.max() <= 1e-2 and err[np.abs(a) > 1e-2].max() <= 1e-4
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
+def test_example_decodes_the_same_in_a_graph(eg, kind):
+    """Five decode steps, the last four replayed: the bits of five eager ones."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_step.py")
+    spec = importlib.util.spec_from_file_location("attention_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    (a, worst), (b, _) = (mod.generate(5, kind, graph) for graph in (True, False))
+    assert worst <= 4 * H and int(a.m.bad) == 0
+    for name in ("cids", "h", "q", "att", "lse"):
+        assert np.array_equal(host(getattr(a, name)), host(getattr(b, name))), name
+    for name in ("history", "live"):
+        assert np.array_equal(host(getattr(a.m, name)), host(getattr(b.m, name))), name
+    with pytest.raises(ValueError, match="places"):
+        mod.generate(1000, kind)
