@@ -243,7 +243,7 @@ struct Work {
   Seen seen;
   int s, pair, kvh, hb, index;             // index: which piece of the run
   int end, c0, c1, tiles, page0, pages;
-  bool whole, first;                       // the piece is its whole pair; the stretch begins it
+  bool whole;                              // the piece is its whole pair
 };
 
 template <int kDb, bool kMx, int kHt>
@@ -274,7 +274,6 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
   auto next_work = [&](Work &w) {
     if (w.c1 < w.end) {
       w.c0 = w.c1;
-      w.first = false;
     } else {
       for (;; ++run.s) {
         if (run.left <= 0) return false;
@@ -289,7 +288,6 @@ __global__ __launch_bounds__(64 * kW, kDb * kHt > 6 ? 1 : 2) void paged_attentio
       run.local += count;
       if (run.local == w.seen.units * pairs) ++run.s, run.local = 0;
       w.whole = count == w.seen.units;
-      w.first = true;
       ++w.index;
       w.kvh = w.pair / sp.head_blocks;
       w.hb = w.pair - w.kvh * sp.head_blocks;

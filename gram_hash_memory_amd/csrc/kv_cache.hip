@@ -32,7 +32,6 @@ struct Row {
   int head;
   bool is_v, first, in;
 };
-template <int LP>
 __device__ __forceinline__ Row row_of(uint32_t row, uint32_t rows, const CacheView &c,
                                       uint32_t recip) {
   const uint32_t heads = 2 * c.kv_heads;           // of a token: the keys', then the values'
@@ -55,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(
   u32x4 w[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    r[i] = row_of<LP>(first + i * kRows, rows, c, recip);
+    r[i] = row_of(first + i * kRows, rows, c, recip);
     slot[i] = -1;
     w[i] = u32x4{};
     if (!r[i].in || 8 * sub >= c.head_dim) continue;
@@ -87,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(
   uint32_t scale[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    r[i] = row_of<LP>(first + i * kRows, rows, c, recip);
+    r[i] = row_of(first + i * kRows, rows, c, recip);
     slot[i] = r[i].in ? slots[r[i].t] : -1;
   }
 #pragma unroll
