@@ -4,9 +4,9 @@
 //   m = max_p scale q.k_p,  lse = m + log sum_p e^(scale q.k_p - m)
 //
 // Bound by reading the seen keys and values once: 64 ragged streams of up to
-// 4096 places in 8 bits, 333 MB, take 67 us (5.0 TB/s) and 5 us to join; one of
+// 4096 places in 8 bits, 333 MB, take 69 us (4.8 TB/s) and 5 us to join; one of
 // 131072 places in bf16, 537 MB, 93 us (5.8 TB/s) and 5.  One of 500 places takes
-// 9.1 us, by latency alone.  The query heads of one key-value head share a
+// 9.3 us, by latency alone.  The query heads of one key-value head share a
 // workgroup (up to 32 of them), so that each key and value is read once.  The
 // work of all sequences is cut into equal runs, a workgroup each (chunks of the
 // longest length instead: 76 to 92 us for the 64 streams); what of a run is not
@@ -23,7 +23,12 @@
 //    are the same 8 places' values of dimension base + w (l % 16) + n, for
 //    n = 0 .. w - 1 in turn: a lane reads w neighbouring dimensions of each
 //    of its 8 places, and an 8 x w transpose between its own registers (one
-//    v_perm for two values) is all that V needs.
+//    v_perm for two values) is all that V needs;
+//  - a weight goes through the matrix cores as the sum of two bf16 values, 2^-15
+//    off at most.  Weights in one bf16 value add 6 to 8 % to the error that the
+//    result's own rounding makes (1.66e-3 of its norm) and save little: the 64
+//    streams take 70.9 instead of 71.9 us, one of 500 places 8.9 instead of 9.3,
+//    64 streams of 32 query heads a key-value head 28.2 instead of 29.4.
 // No lane waits for another in the loop: waves run apart, and the next 32
 // places are requested as soon as a register is free.  The next sequence's
 // first places are requested before this one's results are joined in LDS.

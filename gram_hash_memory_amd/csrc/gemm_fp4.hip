@@ -8,10 +8,12 @@
 // turn, so that a row's next 512 bytes are under way at any time.
 //
 // Bound by reading the weight once where tokens are few (one token of 6144 x
-// 20480: 15.5 us, 4.4 TB/s; of 4096 x 6144: 6.4 us, of which some 4 are launch
-// and two memory latencies).  64 tokens of 6144 x 20480 take 24.6 us (2.9 TB/s,
-// 0.66 PFLOP/s): matrix cores 6 us, conversions 4, the vector cache 9 (every CU
-// pulls all of x), the partial sums 3, in two waves a SIMD that overlap in part.
+// 20480, weights that the last cache does not hold: 16.9 us, 4.0 TB/s; of 4096 x
+// 6144: 6.5 us, of which some 4 are launch and two memory latencies).  64 tokens
+// of 6144 x 20480 take 28.3 us (2.5 TB/s, 0.57 PFLOP/s; 24.8 us where the weight
+// is still in the last cache).  Of those cycles the matrix cores are busy 27 %,
+// the VALU 30 %, LDS 21 %, the vector cache's addressing 61 % and its return path
+// 73 % (every CU pulls all of x), and waves spend 35 % of theirs waiting for data.
 //
 // What the vector cache takes goes by the runs of addresses in 16 neighbouring
 // lanes, a clock each, so neighbouring lanes read neighbouring bytes and LDS
@@ -39,7 +41,9 @@ __device__ __forceinline__ uint32_t e2m1_rne(float x) {
   return code | ((__float_as_uint(x) >> 28) & 8u);
 }
 
-// One thread per block of 32 k: 64 bytes of bf16 in, 16 bytes of codes out.
+// One thread per block of 32 k: 64 bytes of bf16 in, 16 bytes of codes out.  A
+// weight's bytes, once when it is loaded: 20480 x 6144 takes 74 us, 4.3 TB/s of
+// the copy's 5.1; 4096 x 4096 13 us.
 __global__ __launch_bounds__(kThreads) void quantize_fp4_kernel(const uint16_t *__restrict__ w,
                                                                 int64_t blocks,
                                                                 uint8_t *__restrict__ codes,
@@ -372,7 +376,9 @@ struct Tile {
 // The tile with the least to pull through a CU's vector cache: per 32 k a tile
 // takes 64 bytes a token and 17 a column, and the CUs take ceil(tiles / 256)
 // tiles each.  (64 tokens of 6144 x 20480 in tiles of 32 tokens: 36.6 us instead
-// of 28.9.)
+// of 28.9.)  At most 5 x 16 columns, as LDS is full with 64 tokens then: past 256
+// tiles of them some CUs take a second (64 tokens, K 6144: 20480 columns 28.9 us,
+// 20496 41.3, 40960 55.9; 32 tokens: 22.3, 27.8, 40.9).
 Tile pick_tile(int32_t T, int32_t N) {
   Tile best{1, 1};
   int64_t least = INT64_MAX;

@@ -24,8 +24,9 @@ __device__ __forceinline__ int64_t row_index(const CacheView &c, int64_t slot, i
 
 // 16 bytes past the caches where there is much to move once: the stores
 // otherwise push out what is still to be read, and written lines wait in the
-// caches for their turn (32768 tokens read back: 55.3 us with plain stores,
-// 50.7 us so; norm and rotation of 8192 tokens 37.8 and, its loads too, 31.3 us).
+// caches for their turn (8192 tokens written and 32768 read back: 55.3 us with
+// plain stores, 50.7 us so; norm and rotation of 8192 tokens, its loads too: 37.8
+// and 32 us).
 template <bool kOnce>
 __device__ __forceinline__ u32x4 load16(const void *p) {
   if constexpr (kOnce) return __builtin_nontemporal_load(static_cast<const u32x4 *>(p));

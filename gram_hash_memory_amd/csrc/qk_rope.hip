@@ -4,7 +4,7 @@
 //   y = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos - b sin, b cos + a sin)
 //
 // Bound by the bytes of qkv, q and k: 8192 tokens of 32 + 8 heads of 128 take
-// 33 us, 5.1 TB/s.  A wave takes some of a token's heads, LP lanes a head; all
+// 32 us, 5.2 TB/s.  A wave takes some of a token's heads, LP lanes a head; all
 // of its rows are requested before its angles are formed, one a lane: position *
 // inv_freq in fp64, in turns, less the nearest whole number (an angle at
 // position 10^6 in fp32 would be off by 0.06).  A lane holds two pieces of 8

@@ -525,7 +525,8 @@ ENGRAM_API engram_status engram_cache_read(const engram_kv_cache *cache, const i
  *   qkv DEVICE bf16: row t starts at t * qkv_token_stride (values, a multiple
  *   of 8): q_heads queries, kv_heads keys and (needed with a cache) kv_heads
  *   values of head_dim each.  For each head x of queries, in at least fp32, or
- *   of keys, in fp64 (an 8-bit cache rounds their results again):
+ *   of keys, in fp64 (an 8-bit cache rounds their results again; x * weight has
+ *   to lie within fp32's range):
  *     y_i = x_i / sqrt(mean(x^2) + eps) * weight_i;
  *     then dims 0..rotary_dim-1 are rotated in pairs (a, b), pair i by the
  *     angle positions[t] * inv_freq[i] (formed and reduced in fp64):
