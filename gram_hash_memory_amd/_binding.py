@@ -36,7 +36,10 @@ EXPORTS = ("engram_hash", "engram_history_update", "engram_rows", "engram_projec
            "engram_gate_layers", "engram_workspace_bytes", "engram_forward", "engram_last_error",
            "engram_build_id", "engram_forward_noalloc", "engram_cache_write",
            "engram_cache_read", "engram_qk_norm_rope", "engram_paged_attention_workspace_bytes",
-           "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4")
+           "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4",
+           "engram_chunk_attention_workspace_bytes", "engram_chunk_attention",
+           "engram_shared_prefix_attention_workspace_bytes", "engram_shared_prefix_attention",
+           "engram_cache_weights", "engram_cache_evict")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python gram_hash_memory_amd/build.py`")
@@ -87,6 +90,11 @@ class _KVCache(ctypes.Structure):
                 ("k_scales", c_void_p), ("v_scales", c_void_p)]
 
 
+class _AttentionRules(ctypes.Structure):
+    _fields_ = [("window", c_int32), ("cap", c_float), ("slopes", c_void_p),
+                ("doc_starts", c_void_p), ("prefix_lens", c_void_p)]
+
+
 _P = ctypes.POINTER
 _lib.engram_hash.argtypes = [_P(_HashParams), _P(_Tokens), c_void_p, c_void_p]
 _lib.engram_history_update.argtypes = [_P(_Tokens), c_int32, c_void_p, c_void_p, c_void_p]
@@ -135,13 +143,34 @@ _lib.engram_paged_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_int32, c
 _lib.engram_quantize_mxfp4.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]
 _lib.engram_project_mxfp4.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                       c_int32, c_void_p]
+_lib.engram_chunk_attention_workspace_bytes.argtypes = [c_int32] * 6
+_lib.engram_chunk_attention_workspace_bytes.restype = c_size_t
+_lib.engram_chunk_attention.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                        c_void_p, c_int32, c_int32, c_int32, c_void_p, c_float,
+                                        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]
+_lib.engram_shared_prefix_attention_workspace_bytes.argtypes = [c_int32] * 7
+_lib.engram_shared_prefix_attention_workspace_bytes.restype = c_size_t
+_lib.engram_shared_prefix_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
+                                                c_void_p, c_int32, c_int32, c_void_p, c_int32,
+                                                c_void_p, c_int32, c_int32, c_int32, c_float,
+                                                c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                                c_void_p]
+_lib.engram_cache_weights.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                      c_void_p, c_int32, c_int32, c_int32, c_void_p, c_float,
+                                      c_void_p, c_void_p, c_int64, c_void_p, c_void_p]
+_lib.engram_cache_evict.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int32,
+                                    c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                    c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                    c_void_p]
 _lib.engram_last_error.restype = c_char_p
 for _name in ("engram_hash", "engram_history_update", "engram_rows", "engram_project", "engram_project_q2k",
               "engram_project_fp8", "engram_quantize_mxfp8", "engram_project_mxfp8",
               "engram_stage_mxfp8", "engram_project_mxfp8_staged", "engram_gate",
               "engram_gate_layers", "engram_forward", "engram_forward_noalloc",
               "engram_cache_write", "engram_cache_read", "engram_qk_norm_rope",
-              "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4"):
+              "engram_paged_attention", "engram_quantize_mxfp4", "engram_project_mxfp4",
+              "engram_chunk_attention", "engram_shared_prefix_attention", "engram_cache_weights",
+              "engram_cache_evict"):
     getattr(_lib, _name).restype = c_int
 
 
@@ -561,6 +590,143 @@ def engram_paged_attention(cache: KVCache, q, table, lens, max_len: int, scale: 
         _dptr(out, torch.int16, n * heads * D, "out"), _dptr(lse, torch.float32, n * heads, "lse"),
         _dptr(workspace, torch.uint8, 0, "workspace"),
         0 if workspace is None else workspace.numel(),
+        _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
+
+
+class AttentionRules:
+    """engram_attention_rules over GPU tensors (kept alive as long as this object): window and cap
+    (0: none), slopes float32 [q_heads], doc_starts int32 [T], prefix_lens int32 [n_seqs] or None."""
+
+    def __init__(self, window: int = 0, cap: float = 0.0, slopes=None, doc_starts=None,
+                 prefix_lens=None):
+        self._keep = (slopes, doc_starts, prefix_lens)
+        # What a call compares with its own sizes: the tensors' lengths, None where there is none.
+        self.sizes = tuple(None if t is None else t.numel() for t in self._keep)
+        self.c = _AttentionRules(window, cap, _dptr(slopes, torch.float32, 0, "slopes"),
+                                 _dptr(doc_starts, torch.int32, 0, "doc_starts"),
+                                 _dptr(prefix_lens, torch.int32, 0, "prefix_lens"))
+        self.address = ctypes.addressof(self.c)
+
+
+def _rules(rules: AttentionRules | None, heads: int, T: int, n: int) -> int | None:
+    if rules is None:
+        return None
+    for name, size, need in zip(("slopes", "doc_starts", "prefix_lens"), rules.sizes, (heads, T, n)):
+        if size is not None and size < need:
+            raise ValueError(f"{name} has {size} elements, needs {need}")
+    return rules.address
+
+
+def _new_tokens(cache: KVCache, q, cu_seqlens, table):
+    """Sizes of a call over new tokens: T, query heads, sequences, the table's width."""
+    shape, pages = q.shape, table.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [T, q_heads, {cache.head_dim}], got {tuple(shape)}")
+    n = cu_seqlens.numel() - 1
+    if n < 0 or len(pages) != 2 or pages[0] != n:
+        raise ValueError(f"table must be [n_seqs={n}, pages] for cu_seqlens of {n + 1} entries, got {tuple(pages)}")
+    return shape[0], shape[1], n, pages[1]
+
+
+def engram_chunk_attention_workspace_bytes(T: int, n_seqs: int, q_heads: int, kv_heads: int,
+                                           head_dim: int, max_len: int) -> int:
+    return int(_lib.engram_chunk_attention_workspace_bytes(T, n_seqs, q_heads, kv_heads, head_dim,
+                                                           max_len))
+
+
+def engram_chunk_attention(cache: KVCache, q, cu_seqlens, table, lens, max_len: int, scale: float,
+                           out, workspace, rules: AttentionRules | None = None, lse=None,
+                           bad_pages=None, stream=None) -> None:
+    """Attention of several new tokens per sequence: q, out int16 [T, q_heads, head_dim],
+    cu_seqlens int32 [n_seqs + 1], table int32 [n_seqs, pages], lens int32 [n_seqs] (new tokens
+    included), lse float32 [T, q_heads]."""
+    T, heads, n, width = _new_tokens(cache, q, cu_seqlens, table)
+    _check(_lib.engram_chunk_attention(
+        cache.address, _dptr(q, torch.int16, 0, "q"), T, _dptr(cu_seqlens, torch.int32, 0, "cu_seqlens"),
+        _dptr(table, torch.int32, 0, "table"), width, _dptr(lens, torch.int32, n, "lens"), n, heads,
+        max_len, _rules(rules, heads, T, n), scale,
+        _dptr(out, torch.int16, T * heads * cache.head_dim, "out"),
+        _dptr(lse, torch.float32, T * heads, "lse"), _dptr(workspace, torch.uint8, 0, "workspace"),
+        0 if workspace is None else workspace.numel(),
+        _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
+
+
+def engram_shared_prefix_attention_workspace_bytes(n_seqs: int, n_groups: int, q_heads: int,
+                                                   kv_heads: int, head_dim: int, max_prefix: int,
+                                                   max_len: int) -> int:
+    return int(_lib.engram_shared_prefix_attention_workspace_bytes(
+        n_seqs, n_groups, q_heads, kv_heads, head_dim, max_prefix, max_len))
+
+
+def engram_shared_prefix_attention(cache: KVCache, q, cu_groups, prefix_table, prefix_lens,
+                                   max_prefix: int, table, lens, max_len: int, scale: float, out,
+                                   workspace, lse=None, bad_pages=None, stream=None) -> None:
+    """Attention of one new token per sequence, groups of sequences sharing a prefix: q, out int16
+    [n_seqs, q_heads, head_dim], cu_groups int32 [n_groups + 1], prefix_table int32 [n_groups,
+    pages], prefix_lens int32 [n_groups], table int32 [n_seqs, pages] and lens int32 [n_seqs] of
+    the own places, lse float32 [n_seqs, q_heads]."""
+    shape, pages, shared = q.shape, table.shape, prefix_table.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [n_seqs, q_heads, {cache.head_dim}], got {tuple(shape)}")
+    n, heads, D = shape
+    if len(pages) != 2 or pages[0] != n:
+        raise ValueError(f"table must be [n_seqs={n}, pages], got {tuple(pages)}")
+    groups = cu_groups.numel() - 1
+    if groups < 1 or len(shared) != 2 or shared[0] != groups:
+        raise ValueError(f"prefix_table must be [n_groups={groups}, pages] for cu_groups of "
+                         f"{groups + 1} entries, got {tuple(shared)}")
+    _check(_lib.engram_shared_prefix_attention(
+        cache.address, _dptr(q, torch.int16, 0, "q"), _dptr(cu_groups, torch.int32, 0, "cu_groups"),
+        _dptr(prefix_table, torch.int32, 0, "prefix_table"), shared[1],
+        _dptr(prefix_lens, torch.int32, groups, "prefix_lens"), groups, max_prefix,
+        _dptr(table, torch.int32, 0, "table"), pages[1], _dptr(lens, torch.int32, n, "lens"), n,
+        heads, max_len, scale, _dptr(out, torch.int16, n * heads * D, "out"),
+        _dptr(lse, torch.float32, n * heads, "lse"), _dptr(workspace, torch.uint8, 0, "workspace"),
+        0 if workspace is None else workspace.numel(),
+        _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
+
+
+def _weights(cache: KVCache, t, n: int, places: int, name: str):
+    """Pointer and places of a weights tensor [n_seqs, kv_heads, places]."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != cache.kv_heads or t.shape[2] < places:
+        raise ValueError(f"{name} must be [n_seqs={n}, kv_heads={cache.kv_heads}, {places} or more], "
+                         f"got {tuple(t.shape)}")
+    return _dptr(t, torch.float32, 0, name), t.shape[2]
+
+
+def engram_cache_weights(cache: KVCache, q, cu_seqlens, table, lens, max_len: int, scale: float, lse,
+                         weights, rules: AttentionRules | None = None, bad_pages=None,
+                         stream=None) -> None:
+    """The attention weights of the cache's places from new tokens, added to weights float32
+    [n_seqs, kv_heads, max_len or more]; q, cu_seqlens, table, lens and rules as
+    engram_chunk_attention took them, lse float32 [T, q_heads] as it gave it."""
+    T, heads, n, width = _new_tokens(cache, q, cu_seqlens, table)
+    w, stride = _weights(cache, weights, n, max_len, "weights")
+    _check(_lib.engram_cache_weights(
+        cache.address, _dptr(q, torch.int16, 0, "q"), T, _dptr(cu_seqlens, torch.int32, 0, "cu_seqlens"),
+        _dptr(table, torch.int32, 0, "table"), width, _dptr(lens, torch.int32, n, "lens"), n, heads,
+        max_len, _rules(rules, heads, T, n), scale, _dptr(lse, torch.float32, T * heads, "lse"), w,
+        stride, _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
+
+
+def engram_cache_evict(cache: KVCache, table, lens, max_len: int, keep: int, sinks: int, recent: int,
+                       weights, to_table, new_lens, new_weights, kept, bad_pages=None,
+                       stream=None) -> None:
+    """Of each sequence and head the keep places that stay, copied to the pages of to_table int32
+    [n_seqs, pages]: new_lens int32 [n_seqs], new_weights float32 [n_seqs, kv_heads, keep or more],
+    kept int32 [n_seqs, kv_heads, keep]."""
+    n = lens.numel()
+    for t, name in ((table, "table"), (to_table, "to_table")):
+        if t.dim() != 2 or t.shape[0] != n:
+            raise ValueError(f"{name} must be [n_seqs={n}, pages], got {tuple(t.shape)}")
+    w, stride = _weights(cache, weights, n, max_len, "weights")
+    nw, new_stride = _weights(cache, new_weights, n, keep, "new_weights")
+    _check(_lib.engram_cache_evict(
+        cache.address, _dptr(table, torch.int32, 0, "table"), table.shape[1],
+        _dptr(lens, torch.int32, n, "lens"), n, max_len, keep, sinks, recent, w, stride,
+        _dptr(to_table, torch.int32, 0, "to_table"), to_table.shape[1],
+        _dptr(new_lens, torch.int32, n, "new_lens"), nw, new_stride,
+        _dptr(kept, torch.int32, n * cache.kv_heads * max(0, keep), "kept"),
         _dptr(bad_pages, torch.int32, 1, "bad_pages"), _stream(stream)))
 
 

@@ -674,6 +674,61 @@ engram_status check_slots(const int64_t *slots, const int32_t *bad_slots) {
   return ENGRAM_OK;
 }
 
+engram_status check_rules(const engram_attention_rules *r, engram::AttentionRules *view) {
+  *view = engram::AttentionRules{};
+  if (!r) return ENGRAM_OK;
+  REQUIRE(r->window >= 0, "window=%d must not be negative", r->window);
+  REQUIRE(r->cap >= 0.f && r->cap - r->cap == 0.f, "cap must be finite and not negative");
+  REQUIRE((!r->slopes || aligned(r->slopes, 4)) && (!r->doc_starts || aligned(r->doc_starts, 4)) &&
+              (!r->prefix_lens || aligned(r->prefix_lens, 4)),
+          "slopes, doc_starts or prefix_lens misaligned");
+  // A window as long as any context is none.
+  *view = engram::AttentionRules{r->slopes, r->doc_starts, r->prefix_lens,
+                                 r->window >= 1 << 30 ? 0 : r->window, r->cap};
+  return ENGRAM_OK;
+}
+
+// What the calls over new tokens and their sequences have in common.
+engram_status check_sequences(const engram::CacheView &c, int32_t n_seqs, int32_t q_heads, int32_t max_len,
+                              int32_t table_width, float scale) {
+  REQUIRE(n_seqs >= 0 && max_len >= 0 && table_width >= 0,
+          "n_seqs=%d, max_len=%d and table_width=%d must not be negative", n_seqs, max_len,
+          table_width);
+  REQUIRE_SUP(max_len <= 1 << 30, "max_len=%d exceeds %d", max_len, 1 << 30);
+  REQUIRE(q_heads >= 1 && q_heads % c.kv_heads == 0,
+          "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, c.kv_heads);
+  REQUIRE(scale == scale && scale - scale == 0.f, "scale must be finite");
+  return ENGRAM_OK;
+}
+
+engram_status check_table(const int32_t *table, int32_t table_width, const int32_t *lens,
+                          const int32_t *bad_pages) {
+  REQUIRE(lens && aligned(lens, 4), "lens is NULL or misaligned");
+  REQUIRE((table && aligned(table, 4)) || table_width == 0, "table is NULL or misaligned");
+  REQUIRE(!bad_pages || aligned(bad_pages, 4), "bad_pages misaligned");
+  return ENGRAM_OK;
+}
+
+// Bytes of workspace of a chunk (n_groups 0) or of a shared prefix; -1: too much work.
+int64_t tile_workspace(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int32_t kv_heads,
+                       int32_t head_dim, int32_t max_len, int32_t max_prefix) {
+  if (T > 1 << 30 || n_seqs > 1 << 30 || n_groups > 1 << 30 || int64_t(T) * q_heads > int64_t(1) << 40) return -1;
+  return engram::tile_attention_workspace(T, n_seqs, n_groups, q_heads, kv_heads, head_dim, max_len, max_prefix);
+}
+
+engram_status run_tiles(engram::TileAttention &a, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream, const char *what) {
+  const int64_t need = tile_workspace(a.T, a.n_seqs, a.n_groups, a.q_heads, a.cache.kv_heads,
+                                      a.cache.head_dim, a.max_len, a.max_prefix);
+  REQUIRE_SUP(need >= 0, "%d tokens of %d sequences and %d heads over max_len=%d are too many for one call",
+              a.T, a.n_seqs, a.q_heads, std::max(a.max_len, a.max_prefix));
+  REQUIRE(workspace && aligned(workspace, 256), "workspace is NULL or not 256-byte aligned");
+  REQUIRE(workspace_bytes >= size_t(need), "workspace_bytes=%zu < required %lld", workspace_bytes,
+          (long long)need);
+  a.workspace = workspace;
+  return hip_status(engram::launch_tile_attention(a, stream), what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -840,6 +895,202 @@ engram_status engram_paged_attention(const engram_kv_cache *cache, const uint16_
               "n_seqs=%d of %d heads over max_len=%d are too many for one call", n_seqs, q_heads,
               max_len);
   return hip_status(engram::launch_paged_attention(a, stream), "engram_paged_attention launch");
+}
+
+size_t engram_chunk_attention_workspace_bytes(int32_t T, int32_t n_seqs, int32_t q_heads,
+                                              int32_t kv_heads, int32_t head_dim, int32_t max_len) {
+  if (T <= 0 || n_seqs <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 ||
+      !head_dim_ok(head_dim) || max_len < 0 || max_len > 1 << 30)
+    return 0;
+  return size_t(std::max<int64_t>(0, tile_workspace(T, n_seqs, 0, q_heads, kv_heads, head_dim, max_len, 0)));
+}
+
+engram_status engram_chunk_attention(const engram_kv_cache *cache, const uint16_t *q, int32_t T,
+                                     const int32_t *cu_seqlens, const int32_t *table,
+                                     int32_t table_width, const int32_t *lens, int32_t n_seqs,
+                                     int32_t q_heads, int32_t max_len,
+                                     const engram_attention_rules *rules, float scale,
+                                     uint16_t *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, int32_t *bad_pages,
+                                     hipStream_t stream) {
+  engram::TileAttention a{};
+  engram_status st = check_cache(cache, &a.cache);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  if ((st = check_sequences(a.cache, n_seqs, q_heads, max_len, table_width, scale)) != ENGRAM_OK) return st;
+  if ((st = check_rules(rules, &a.rules)) != ENGRAM_OK) return st;
+  if (T == 0 || n_seqs == 0) return ENGRAM_OK;
+  REQUIRE(q && out && aligned(q, 16) && aligned(out, 16),
+          "q or out is NULL or not 16-byte aligned");
+  REQUIRE(cu_seqlens && aligned(cu_seqlens, 4), "cu_seqlens is NULL or misaligned");
+  if ((st = check_table(table, table_width, lens, bad_pages)) != ENGRAM_OK) return st;
+  REQUIRE(!lse || aligned(lse, 4), "lse misaligned");
+  a.q = q;
+  a.T = T;
+  a.cu = cu_seqlens;
+  a.table = table;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.n_seqs = n_seqs;
+  a.q_heads = q_heads;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.bad_pages = bad_pages;
+  return run_tiles(a, workspace, workspace_bytes, stream, "engram_chunk_attention launch");
+}
+
+size_t engram_shared_prefix_attention_workspace_bytes(int32_t n_seqs, int32_t n_groups,
+                                                      int32_t q_heads, int32_t kv_heads,
+                                                      int32_t head_dim, int32_t max_prefix,
+                                                      int32_t max_len) {
+  if (n_seqs <= 0 || n_groups <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 ||
+      !head_dim_ok(head_dim) || max_len < 0 || max_len > 1 << 30 || max_prefix < 0 ||
+      max_prefix > 1 << 30)
+    return 0;
+  return size_t(std::max<int64_t>(0, tile_workspace(n_seqs, n_seqs, n_groups, q_heads, kv_heads,
+                                                    head_dim, max_len, max_prefix)));
+}
+
+engram_status engram_shared_prefix_attention(
+    const engram_kv_cache *cache, const uint16_t *q, const int32_t *cu_groups,
+    const int32_t *prefix_table, int32_t prefix_width, const int32_t *prefix_lens,
+    int32_t n_groups, int32_t max_prefix, const int32_t *table, int32_t table_width,
+    const int32_t *lens, int32_t n_seqs, int32_t q_heads, int32_t max_len, float scale,
+    uint16_t *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *bad_pages,
+    hipStream_t stream) {
+  engram::TileAttention a{};
+  engram_status st = check_cache(cache, &a.cache);
+  if (st != ENGRAM_OK) return st;
+  if ((st = check_sequences(a.cache, n_seqs, q_heads, max_len, table_width, scale)) != ENGRAM_OK) return st;
+  REQUIRE(n_groups >= 1 && max_prefix >= 0 && prefix_width >= 1,
+          "n_groups=%d and prefix_width=%d must be positive, max_prefix=%d not negative", n_groups,
+          prefix_width, max_prefix);
+  REQUIRE_SUP(max_prefix <= 1 << 30, "max_prefix=%d exceeds %d", max_prefix, 1 << 30);
+  if (n_seqs == 0) return ENGRAM_OK;
+  REQUIRE(q && out && aligned(q, 16) && aligned(out, 16),
+          "q or out is NULL or not 16-byte aligned");
+  REQUIRE(cu_groups && aligned(cu_groups, 4), "cu_groups is NULL or misaligned");
+  if ((st = check_table(table, table_width, lens, bad_pages)) != ENGRAM_OK) return st;
+  REQUIRE(prefix_table && prefix_lens && aligned(prefix_table, 4) && aligned(prefix_lens, 4),
+          "prefix_table or prefix_lens is NULL or misaligned");
+  REQUIRE(!lse || aligned(lse, 4), "lse misaligned");
+  a.q = q;
+  a.T = n_seqs;
+  a.cu = cu_groups;
+  a.prefix_table = prefix_table;
+  a.prefix_width = prefix_width;
+  a.prefix_lens = prefix_lens;
+  a.n_groups = n_groups;
+  a.max_prefix = max_prefix;
+  a.table = table;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.n_seqs = n_seqs;
+  a.q_heads = q_heads;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.bad_pages = bad_pages;
+  return run_tiles(a, workspace, workspace_bytes, stream, "engram_shared_prefix_attention launch");
+}
+
+engram_status engram_cache_weights(const engram_kv_cache *cache, const uint16_t *q, int32_t T,
+                                   const int32_t *cu_seqlens, const int32_t *table,
+                                   int32_t table_width, const int32_t *lens, int32_t n_seqs,
+                                   int32_t q_heads, int32_t max_len,
+                                   const engram_attention_rules *rules, float scale,
+                                   const float *lse, float *weights, int64_t weights_stride,
+                                   int32_t *bad_pages, hipStream_t stream) {
+  engram::CacheWeights a{};
+  engram_status st = check_cache(cache, &a.cache);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(T >= 0, "T=%d < 0", T);
+  REQUIRE_SUP(T <= 1 << 30 && int64_t(T) * (q_heads / a.cache.kv_heads) <= 1 << 30,
+              "T=%d tokens of %d heads are too many for one call", T, q_heads);
+  if ((st = check_sequences(a.cache, n_seqs, q_heads, max_len, table_width, scale)) != ENGRAM_OK) return st;
+  if ((st = check_rules(rules, &a.rules)) != ENGRAM_OK) return st;
+  REQUIRE(weights_stride >= max_len, "weights_stride=%lld must be at least max_len=%d",
+          (long long)weights_stride, max_len);
+  if (T == 0 || n_seqs == 0 || max_len == 0) return ENGRAM_OK;
+  REQUIRE_SUP(engram::cache_weights_blocks(n_seqs, a.cache.kv_heads, max_len) <= kMaxBlocks,
+              "n_seqs=%d over max_len=%d are too many for one call", n_seqs, max_len);
+  REQUIRE(q && aligned(q, 16), "q is NULL or not 16-byte aligned");
+  REQUIRE(cu_seqlens && aligned(cu_seqlens, 4), "cu_seqlens is NULL or misaligned");
+  if ((st = check_table(table, table_width, lens, bad_pages)) != ENGRAM_OK) return st;
+  REQUIRE(lse && weights && aligned(lse, 4) && aligned(weights, 4),
+          "lse or weights is NULL or misaligned");
+  a.q = q;
+  a.T = T;
+  a.cu = cu_seqlens;
+  a.table = table;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.n_seqs = n_seqs;
+  a.q_heads = q_heads;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.lse = lse;
+  a.weights = weights;
+  a.weights_stride = weights_stride;
+  a.bad_pages = bad_pages;
+  return hip_status(engram::launch_cache_weights(a, stream), "engram_cache_weights launch");
+}
+
+engram_status engram_cache_evict(const engram_kv_cache *cache, const int32_t *table,
+                                 int32_t table_width, const int32_t *lens, int32_t n_seqs,
+                                 int32_t max_len, int32_t keep, int32_t sinks, int32_t recent,
+                                 const float *weights, int64_t weights_stride,
+                                 const int32_t *to_table, int32_t to_width, int32_t *new_lens,
+                                 float *new_weights, int64_t new_weights_stride, int32_t *kept,
+                                 int32_t *bad_pages, hipStream_t stream) {
+  engram::CacheEvict a{};
+  engram_status st = check_cache(cache, &a.cache);
+  if (st != ENGRAM_OK) return st;
+  REQUIRE(n_seqs >= 0 && max_len >= 0 && table_width >= 0 && to_width >= 0,
+          "n_seqs=%d, max_len=%d, table_width=%d and to_width=%d must not be negative", n_seqs,
+          max_len, table_width, to_width);
+  REQUIRE_SUP(max_len <= 1 << 30 && keep <= 1 << 30, "max_len=%d or keep=%d exceeds %d", max_len,
+              keep, 1 << 30);
+  REQUIRE(keep >= 0 && sinks >= 0 && recent >= 0 && int64_t(sinks) + recent <= keep,
+          "sinks=%d and recent=%d must not be negative, nor more than keep=%d", sinks, recent, keep);
+  REQUIRE(int64_t(to_width) * cache->page_size >= keep,
+          "to_width=%d pages of %d places are fewer than keep=%d", to_width, cache->page_size, keep);
+  REQUIRE(weights_stride >= max_len && new_weights_stride >= keep,
+          "weights_stride=%lld must be at least max_len=%d, new_weights_stride=%lld at least keep=%d",
+          (long long)weights_stride, max_len, (long long)new_weights_stride, keep);
+  if (n_seqs == 0) return ENGRAM_OK;
+  REQUIRE_SUP(int64_t(n_seqs) * a.cache.kv_heads <= kMaxBlocks / 4 &&
+                  engram::cache_evict_blocks(a.cache, n_seqs, keep) <= kMaxBlocks,
+              "n_seqs=%d of %d heads and keep=%d are too many for one call", n_seqs,
+              a.cache.kv_heads, keep);
+  if ((st = check_table(table, table_width, lens, bad_pages)) != ENGRAM_OK) return st;
+  REQUIRE((to_table && aligned(to_table, 4)) || keep == 0, "to_table is NULL or misaligned");
+  REQUIRE((weights && aligned(weights, 4)) || max_len == 0, "weights is NULL or misaligned");
+  REQUIRE(new_lens && aligned(new_lens, 4), "new_lens is NULL or misaligned");
+  REQUIRE((new_weights && aligned(new_weights, 4)) || new_weights_stride == 0,
+          "new_weights is NULL or misaligned");
+  REQUIRE((kept && aligned(kept, 4)) || keep == 0, "kept is NULL or misaligned");
+  a.table = table;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.n_seqs = n_seqs;
+  a.max_len = max_len;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.weights = weights;
+  a.weights_stride = weights_stride;
+  a.to_table = to_table;
+  a.to_width = to_width;
+  a.new_lens = new_lens;
+  a.new_weights = new_weights;
+  a.new_weights_stride = new_weights_stride;
+  a.kept = kept;
+  a.bad_pages = bad_pages;
+  return hip_status(engram::launch_cache_evict(a, stream), "engram_cache_evict launch");
 }
 
 engram_status engram_quantize_mxfp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,

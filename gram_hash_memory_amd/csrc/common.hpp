@@ -201,6 +201,65 @@ int64_t paged_attention_workspace(int32_t n_seqs, int32_t q_heads, int32_t kv_he
 int64_t paged_attention_units(int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len);
 hipError_t launch_paged_attention(const PagedAttention &a, hipStream_t stream);
 
+// Which places a new token sees, and what happens to its scores (device pointers
+// may be NULL; cap 0: none).
+struct AttentionRules {
+  const float *slopes;
+  const int32_t *doc_starts, *prefix_lens;
+  int32_t window;
+  float cap;
+};
+
+// Attention of several query rows a key-value head (chunk_attention.hip).  With
+// prefix_table the sequences have one new token each, cu cuts them into groups,
+// and a group shares the prefix_lens[g] places of row g of prefix_table; else cu
+// cuts the T tokens into sequences.
+struct TileAttention {
+  CacheView cache;
+  AttentionRules rules;
+  const uint16_t *q;
+  const int32_t *cu, *table, *lens, *prefix_table, *prefix_lens;
+  uint16_t *out;
+  float *lse;
+  void *workspace;
+  int32_t *bad_pages;
+  int32_t T, n_seqs, n_groups, q_heads, table_width, prefix_width, max_len, max_prefix;
+  float scale;
+};
+// Bytes, for a call over T tokens (n_groups 0: a chunk); -1 where the work is
+// counted past 31 bits.
+int64_t tile_attention_workspace(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads,
+                                 int32_t kv_heads, int32_t head_dim, int32_t max_len,
+                                 int32_t max_prefix);
+hipError_t launch_tile_attention(const TileAttention &a, hipStream_t stream);
+
+struct CacheWeights {
+  CacheView cache;
+  AttentionRules rules;
+  const uint16_t *q;
+  const int32_t *cu, *table, *lens;
+  const float *lse;
+  float *weights;
+  int32_t *bad_pages;
+  int64_t weights_stride;        // of a (sequence, head)
+  int32_t T, n_seqs, q_heads, table_width, max_len;
+  float scale;
+};
+int64_t cache_weights_blocks(int32_t n_seqs, int32_t kv_heads, int32_t max_len);
+hipError_t launch_cache_weights(const CacheWeights &a, hipStream_t stream);
+
+struct CacheEvict {
+  CacheView cache;
+  const int32_t *table, *lens, *to_table;
+  const float *weights;
+  float *new_weights;
+  int32_t *new_lens, *kept, *bad_pages;
+  int64_t weights_stride, new_weights_stride;
+  int32_t n_seqs, table_width, to_width, max_len, keep, sinks, recent;
+};
+int64_t cache_evict_blocks(const CacheView &c, int32_t n_seqs, int32_t keep);
+hipError_t launch_cache_evict(const CacheEvict &a, hipStream_t stream);
+
 hipError_t launch_quantize_fp4(const uint16_t *w, int32_t N, int32_t K, uint8_t *codes,
                                uint8_t *scales, hipStream_t stream);
 int64_t project_fp4_blocks(int32_t T, int32_t N);       // workgroups of 512 threads

@@ -459,9 +459,10 @@ ENGRAM_API engram_status engram_forward_noalloc(const engram_hash_params *params
 /* ------------------------------------------------------------------------
  * The decoder layer's attention step, for programs that stream tokens through
  * a layer beside the Engram forward: per-head norms and rotation of queries
- * and keys, a paged key-value cache in bf16 or in 8 bits, attention of one new
- * token per sequence over it, and the projection of few tokens by a 4-bit
- * weight.  Conventions as above.
+ * and keys, a paged key-value cache in bf16 or in 8 bits, attention over it (of
+ * one new token per sequence, of several, of sequences that share a prefix), its
+ * places' attention weights and eviction by them, and the projection of few
+ * tokens by a 4-bit weight.  Conventions as above.
  * ------------------------------------------------------------------------ */
 
 typedef enum engram_cache_format ENGRAM_ENUM_BASE {
@@ -592,6 +593,128 @@ ENGRAM_API engram_status engram_paged_attention(const engram_kv_cache *cache, co
                                                 int32_t window, uint16_t *out, float *lse,
                                                 void *workspace, size_t workspace_bytes,
                                                 int32_t *bad_pages, hipStream_t stream);
+
+/* Which places a new token sees, and what becomes of its scores, for
+ * engram_chunk_attention and engram_cache_weights.  A HOST struct, read during
+ * the call; NULL stands for all zero: places up to the token's own, plain scores.
+ *   window: places that a token sees, its own included (0: all up to its own).
+ *   cap: scores become cap * tanh(score / cap) (0: they stay).
+ *   slopes DEVICE fp32 [q_heads] or NULL: slopes[h] * |distance in places| is
+ *        then taken off.
+ *   doc_starts DEVICE int32 [T] or NULL: the place where a new token's document
+ *        begins; it sees no place before that.  (A padding token is given a place
+ *        behind the sequence, 2^31 - 1 say, and sees nothing.)
+ *   prefix_lens DEVICE int32 [n_seqs] or NULL: places 0 .. prefix_lens[s] - 1 are
+ *        seen by all of sequence s's tokens, later or earlier and past any window
+ *        (within their documents and the sequence's length).
+ */
+typedef struct engram_attention_rules {
+  int32_t window;
+  float cap;
+  const float *slopes;
+  const int32_t *doc_starts;
+  const int32_t *prefix_lens;
+} engram_attention_rules;
+
+/* Bytes of device workspace engram_chunk_attention needs (0: sizes that the call
+ * refuses, or nothing to do). */
+ENGRAM_API size_t engram_chunk_attention_workspace_bytes(int32_t T, int32_t n_seqs,
+                                                         int32_t q_heads, int32_t kv_heads,
+                                                         int32_t head_dim, int32_t max_len);
+
+/* Attention of several new tokens per sequence over the paged cache, which holds
+ * their keys and values already: prompts, chunks of them, drafts, single tokens.
+ *   q DEVICE bf16 [T][q_heads][head_dim]; sequence s's new tokens are rows
+ *   cu_seqlens[s] .. cu_seqlens[s+1]-1 (DEVICE int32 [n_seqs+1], nondecreasing,
+ *   within 0..T; rows outside them are neither read nor written).  lens[s]
+ *   counts all of its places, the new tokens' included: of n new tokens the i-th
+ *   is at place lens[s] - n + i.  table, lens, max_len, q_heads, scale and
+ *   bad_pages as for engram_paged_attention.
+ *     score(t, p) = scale q.k_p, then as `rules` says;
+ *     out = sum_p exp(score) v_p / sum_p exp(score) over the places seen, in bf16;
+ *     lse (DEVICE fp32 [T][q_heads], nullable) = log sum_p exp(score).
+ *   Where nothing is seen out is 0 and lse -infinity.  A place has no effect on
+ *   rows that do not see it, whatever it holds.  Scores, softmax statistics and
+ *   sums are held in fp32; a weight exp(.) is rounded to bf16 for the matrix cores.
+ *   Results do not depend on timing.
+ *   Limits: T and max_len at most 2^30; with B blocks of 128 rows (T * q_heads /
+ *   kv_heads / 128 + n_seqs), B * (max_len / 64 + 2) * kv_heads below 2^28.
+ *   workspace DEVICE, 256-byte aligned; its contents are scratch.
+ */
+ENGRAM_API engram_status engram_chunk_attention(
+    const engram_kv_cache *cache, const uint16_t *q, int32_t T, const int32_t *cu_seqlens,
+    const int32_t *table, int32_t table_width, const int32_t *lens, int32_t n_seqs,
+    int32_t q_heads, int32_t max_len, const engram_attention_rules *rules, float scale,
+    uint16_t *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *bad_pages,
+    hipStream_t stream);
+
+ENGRAM_API size_t engram_shared_prefix_attention_workspace_bytes(
+    int32_t n_seqs, int32_t n_groups, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+    int32_t max_prefix, int32_t max_len);
+
+/* Attention of one new token per sequence, where sequences share a prefix: the
+ * prefix is read once for all of them.
+ *   Sequences cu_groups[g] .. cu_groups[g+1]-1 (DEVICE int32 [n_groups+1],
+ *   nondecreasing, within 0..n_seqs) see the prefix_lens[g] places of row g of
+ *   prefix_table (DEVICE int32 [n_groups][prefix_width]; lengths counted as
+ *   engram_paged_attention counts lens, with max_prefix), and each its own
+ *   lens[s] places of row s of table (lens[s] = 0: the prefix only).  A sequence
+ *   of no group has its own places only.  q, out, lse, scale and bad_pages as for
+ *   engram_paged_attention; results are those of that call over the prefix's
+ *   places followed by the own ones (weights are rounded as in
+ *   engram_chunk_attention).  n_groups >= 1.
+ *   Limits as for engram_chunk_attention, with T = n_seqs and n_groups + n_seqs
+ *   more blocks, and n_seqs * q_heads below 2^30.
+ */
+ENGRAM_API engram_status engram_shared_prefix_attention(
+    const engram_kv_cache *cache, const uint16_t *q, const int32_t *cu_groups,
+    const int32_t *prefix_table, int32_t prefix_width, const int32_t *prefix_lens,
+    int32_t n_groups, int32_t max_prefix, const int32_t *table, int32_t table_width,
+    const int32_t *lens, int32_t n_seqs, int32_t q_heads, int32_t max_len, float scale,
+    uint16_t *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *bad_pages,
+    hipStream_t stream);
+
+/* The attention weight that the cache's places get from new tokens, added up:
+ *     weights[s][kvh][p] += sum of exp(score(t, p) - lse[t][h]) over sequence s's
+ *     new tokens t and the query heads h of key-value head kvh that see place p,
+ *   with q, cu_seqlens, table, lens, rules and scale as engram_chunk_attention took
+ *   them, or engram_paged_attention for one new token each (cu_seqlens[s] = s), and
+ *   the lse that it gave (DEVICE fp32 [T][q_heads]; -infinity: a row without
+ *   weights).  weights DEVICE fp32 [n_seqs][kv_heads][weights_stride],
+ *   weights_stride >= max_len; places from lens[s] on are not touched.  fp32
+ *   throughout, in an order that does not depend on timing.
+ */
+ENGRAM_API engram_status engram_cache_weights(
+    const engram_kv_cache *cache, const uint16_t *q, int32_t T, const int32_t *cu_seqlens,
+    const int32_t *table, int32_t table_width, const int32_t *lens, int32_t n_seqs,
+    int32_t q_heads, int32_t max_len, const engram_attention_rules *rules, float scale,
+    const float *lse, float *weights, int64_t weights_stride, int32_t *bad_pages,
+    hipStream_t stream);
+
+/* Eviction: of each sequence and key-value head the `keep` places that stay, copied
+ * in their order to other pages of the same cache.
+ *   A sequence of more than keep places keeps, of each head, its first `sinks` and
+ *   its last `recent` places and of the others those of largest weight (NaN below
+ *   all numbers; of equal ones the first); a shorter one keeps all.  sinks + recent
+ *   <= keep.  table, lens and max_len as for engram_paged_attention; weights DEVICE
+ *   fp32 [n_seqs][kv_heads][weights_stride], weights_stride >= max_len.
+ *   Kept place i goes to place i of row s of to_table (DEVICE int32
+ *   [n_seqs][to_width], to_width * page_size >= keep), heads apart, bit for bit: its
+ *   pages must be distinct, and in no row of table (other sequences may share the
+ *   old pages).  new_lens DEVICE int32 [n_seqs] = min(length, keep); new_weights
+ *   DEVICE fp32 [n_seqs][kv_heads][new_weights_stride], new_weights_stride >= keep:
+ *   the kept places' weights, then 0; kept DEVICE int32 [n_seqs][kv_heads][keep]:
+ *   the kept places, then -1.  Outputs must not overlap the inputs.
+ *   A kept place on a page outside the cache becomes zeros, one that goes to such a
+ *   page is not written; bad_pages (nullable) is incremented at least once for
+ *   either.
+ */
+ENGRAM_API engram_status engram_cache_evict(
+    const engram_kv_cache *cache, const int32_t *table, int32_t table_width,
+    const int32_t *lens, int32_t n_seqs, int32_t max_len, int32_t keep, int32_t sinks,
+    int32_t recent, const float *weights, int64_t weights_stride, const int32_t *to_table,
+    int32_t to_width, int32_t *new_lens, float *new_weights, int64_t new_weights_stride,
+    int32_t *kept, int32_t *bad_pages, hipStream_t stream);
 
 /* MXFP4 copy of a bf16 weight, for engram_project_mxfp4 (OCP MX v1.0, E2M1).
  *   w DEVICE bf16 [N][K], K % 32 == 0; codes DEVICE [N][K/2], 16-byte aligned:

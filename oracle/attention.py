@@ -135,3 +135,170 @@ def project_mxfp4(x_bits, codes, scales):
     """(float64 out [T, N], float64 sums of the products' magnitudes)."""
     x, w = bf16_value(x_bits), mxfp4_values(codes, scales)
     return x @ w.T, np.abs(x) @ np.abs(w).T
+
+
+# ---------------------------------------------------------------- several new tokens, shared prefixes, eviction
+
+U32 = 2.0 ** -24                                       # half a step of fp32
+
+
+def rules_of(window=0, cap=0.0, slopes=None, doc_starts=None, prefix_lens=None):
+    return dict(window=window, cap=cap, slopes=slopes, doc_starts=doc_starts, prefix_lens=prefix_lens)
+
+
+def _places(cache, table_row, length):
+    """Keys and values float64 [hkv, L, D] of the places 0..length-1, and which lie on a page of the cache."""
+    k, v, ks, vs = cache
+    pages, _, ps, _ = k.shape
+    p = np.arange(length)
+    page = np.asarray(table_row)[p // ps].astype(np.int64) if length else p
+    ok = (page >= 0) & (page < pages)
+    slots = np.where(ok, page, 0) * ps + p % ps
+    return (cache_rows(k, ks, slots).transpose(1, 0, 2), cache_rows(v, vs, slots).transpose(1, 0, 2), ok)
+
+
+def _scores(q, k, scale, rules, pos, h):
+    """Scores [n, L] of one head's new tokens at places pos, and how far fp32 ones may be off:
+    D roundings in the product, some in the cap (2^-21 of it at most) and the bias."""
+    p = np.arange(k.shape[0])
+    with np.errstate(invalid="ignore", over="ignore"):
+        z = q @ k.T * scale
+        mag = np.abs(q) @ np.abs(k).T * abs(scale)
+    off = U32 * (q.shape[1] + 4) * mag
+    if rules["cap"]:
+        z = rules["cap"] * np.tanh(z / rules["cap"])
+        off = off + 2.0 ** -21 * np.minimum(rules["cap"], mag)
+    if rules["slopes"] is not None:
+        bias = float(rules["slopes"][h]) * np.abs(pos[:, None] - p)
+        z, off = z - bias, off + 4 * U32 * (np.abs(bias) + np.abs(z))
+    return z, off
+
+
+def _seen(rules, s, tokens, pos, length, ok):
+    p = np.arange(length)
+    seen = p <= pos[:, None]
+    if rules["window"]:
+        seen &= pos[:, None] - p < rules["window"]
+    if rules["prefix_lens"] is not None:
+        seen |= p < int(rules["prefix_lens"][s])
+    if rules["doc_starts"] is not None:
+        seen &= p >= np.asarray(rules["doc_starts"])[tokens][:, None].astype(np.int64)
+    return seen & ok
+
+
+def _softmax_row(z, off, seen, v):
+    """out, lse, sum w |v|, and the bounds that `off` gives: of out [n, D] and of lse [n]."""
+    n, D = z.shape[0], v.shape[1]
+    z = np.where(seen, z, -np.inf)
+    some = seen.any(1)
+    top = np.where(some, z.max(1, initial=-np.inf), 0.0)
+    e = np.exp(z - top[:, None])
+    total = e.sum(1)
+    w = np.divide(e, total[:, None], out=np.zeros_like(e), where=total[:, None] > 0)
+    lse = np.full(n, -np.inf)
+    lse[some] = top[some] + np.log(total[some])
+    used = seen.any(0)                                 # what no row sees may be anything
+    w, v, off = w[:, used], v[used], np.where(seen, off, 0.0)[:, used]
+    # A place that one row does not see may hold NaN that another sees.
+    odd = ~np.isfinite(v)
+    fine, weight = np.where(odd, 0.0, v), np.where(seen[:, used], w, 0.0)
+    out, spread = weight @ fine, weight @ np.abs(fine)
+    slack = (weight * off) @ np.abs(fine) + (weight * off).sum(1)[:, None] * np.abs(out)
+    if odd.any():
+        out = np.where((seen[:, used].astype(float) @ odd) > 0, np.nan, out)
+    return out.reshape(n, D), lse, spread, slack, (weight * off).sum(1)
+
+
+def chunk_attention(cache, q_bits, cu, table, lens, max_len, scale, rules=None):
+    """(out, lse, spread, slack, lse_slack) of the tokens in cu; float64 [T, hq, D] or [T, hq]."""
+    rules = rules or rules_of()
+    hkv, ps = cache[0].shape[1:3]
+    T, hq, D = q_bits.shape
+    q = bf16_value(q_bits)
+    out, spread, slack = np.zeros((T, hq, D)), np.zeros((T, hq, D)), np.zeros((T, hq, D))
+    lse, lse_slack = np.full((T, hq), -np.inf), np.zeros((T, hq))
+    for s in range(len(lens)):
+        tokens = np.arange(cu[s], cu[s + 1])
+        length = min(max(int(lens[s]), 0), max_len, table.shape[1] * ps)
+        if not len(tokens) or not length:
+            continue
+        pos = length - len(tokens) + np.arange(len(tokens))
+        k, v, ok = _places(cache, table[s], length)
+        seen = _seen(rules, s, tokens, pos, length, ok)
+        for h in range(hq):
+            kk = np.where(seen.any(0)[:, None], k[h // (hq // hkv)], 0.0)
+            z, off = _scores(q[tokens, h], kk, scale, rules, pos, h)
+            got = _softmax_row(z, off, seen, v[h // (hq // hkv)])
+            for a, x in zip((out, lse, spread, slack, lse_slack), got):
+                a[tokens, h] = x
+    return out, lse, spread, slack, lse_slack
+
+
+def shared_prefix_attention(cache, q_bits, cu_groups, prefix_table, prefix_lens, max_prefix, table, lens, max_len, scale):
+    """chunk_attention's results for one new token a sequence over its group's prefix and its own places."""
+    hkv, ps = cache[0].shape[1:3]
+    n, hq, D = q_bits.shape
+    q = bf16_value(q_bits)
+    got = [np.zeros((n, hq, D)), np.full((n, hq), -np.inf), np.zeros((n, hq, D)), np.zeros((n, hq, D)), np.zeros((n, hq))]
+    prefix = [_places(cache, prefix_table[g], min(max(int(prefix_lens[g]), 0), max_prefix, prefix_table.shape[1] * ps))
+              for g in range(len(prefix_lens))]
+    for s in range(n):
+        k, v, ok = _places(cache, table[s], min(max(int(lens[s]), 0), max_len, table.shape[1] * ps))
+        for g in range(len(prefix_lens)):
+            if cu_groups[g] <= s < cu_groups[g + 1]:
+                k0, v0, ok0 = prefix[g]
+                k, v, ok = np.concatenate([k0, k], 1), np.concatenate([v0, v], 1), np.concatenate([ok0, ok])
+        if not len(ok):
+            continue
+        for h in range(hq):
+            kk = np.where(ok[:, None], k[h // (hq // hkv)], 0.0)
+            z, off = _scores(q[s, h][None], kk, scale, rules_of(), np.zeros(1), h)
+            for a, x in zip(got, _softmax_row(z, off, ok[None], v[h // (hq // hkv)])):
+                a[s, h] = x[0]
+    return got
+
+
+def cache_weights(cache, q_bits, cu, table, lens, max_len, scale, lse, stride, rules=None):
+    """(weights added [n, hkv, stride], how far fp32 ones may be off)."""
+    rules = rules or rules_of()
+    hkv, ps = cache[0].shape[1:3]
+    hq = q_bits.shape[1]
+    q = bf16_value(q_bits)
+    w, slack = np.zeros((len(lens), hkv, stride)), np.zeros((len(lens), hkv, stride))
+    for s in range(len(lens)):
+        tokens = np.arange(cu[s], cu[s + 1])
+        length = min(max(int(lens[s]), 0), max_len, table.shape[1] * ps)
+        if not len(tokens) or not length:
+            continue
+        pos = length - len(tokens) + np.arange(len(tokens))
+        k, _, ok = _places(cache, table[s], length)
+        seen = _seen(rules, s, tokens, pos, length, ok)
+        for h in range(hq):
+            kvh = h // (hq // hkv)
+            z, off = _scores(q[tokens, h], np.where(seen.any(0)[:, None], k[kvh], 0.0), scale, rules, pos, h)
+            ref = np.asarray(lse, np.float64)[tokens, h][:, None]
+            seen_h = seen & ~np.isneginf(ref)
+            e = np.where(seen_h, np.exp(np.where(seen_h, z - np.where(np.isneginf(ref), 0, ref), 0.0)), 0.0)
+            off = np.where(seen_h, off + 4 * U32 * (np.abs(z) + np.abs(np.where(np.isneginf(ref), 0, ref))), 0.0)
+            w[s, kvh, :length] += e.sum(0)
+            # Exponentials (2 u), and the sums of the rows of 16 lanes, then of those.
+            slack[s, kvh, :length] += (e * (off + (8 + len(tokens) * (hq // hkv) / 16) * U32)).sum(0)
+    return w, slack
+
+
+def evict(weights, lens, max_len, room, keep, sinks, recent):
+    """kept int32 [n, hkv, keep]: the places that stay, in order, then -1."""
+    n, hkv, _ = weights.shape
+    kept = np.full((n, hkv, keep), -1, np.int32)
+    for s in range(n):
+        length = min(max(int(lens[s]), 0), max_len, room)
+        for h in range(hkv):
+            p = np.arange(length)
+            if length > keep:
+                w = weights[s, h, :length].astype(np.float64)
+                must = (p < sinks) | (p >= length - recent)
+                # Those that stay anyway, then numbers before NaN, then larger before smaller, then the first.
+                order = np.lexsort((p, np.where(np.isnan(w), 0.0, -w), np.isnan(w), ~must))
+                p = np.sort(order[:keep])
+            kept[s, h, :len(p)] = p
+    return kept
