@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libengram.so")
 SOURCES = ["api.cpp", "hash.hip", "rows.hip", "gemm.hip", "gemm_skinny.hip", "gemm_q2k.hip",
            "gemm_fp8.hip", "gemm_mx.hip", "mx_quant.hip", "gate.hip", "kv_cache.hip", "qk_rope.hip",
-           "attention.hip", "chunk_attention.hip", "cache_weights.hip", "cache_evict.hip", "gemm_fp4.hip"]
+           "attention.hip", "tile_plan.hip", "tile_wide.hip", "tile_narrow.hip", "cache_weights.hip", "cache_evict.hip", "gemm_fp4.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

@@ -34,20 +34,18 @@
 // first places are requested before this one's results are joined in LDS.
 #include <algorithm>
 
+#include "attention_common.hpp"
 #include "attention_lds.hpp"
-#include "kv_cache.hpp"
 
 namespace engram {
 namespace {
 
-using attn::kHeadBlock;
-using attn::kW;
+using namespace attn;
 
 constexpr int kTile = 32;                  // places a wave takes at a time
 constexpr int kUnit = kTile * kW;          // places the work is dealt out by
 constexpr int kMaxChunk = 4096;            // places whose pages are held in LDS at a time
 constexpr int kMinPage = 8;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- the plan
 
@@ -101,72 +99,6 @@ struct Split {
   bool direct;
 };
 
-// How the head_dim = 32 * kDb dimensions fall to 16 lanes: pieces of 16, 8, 4,
-// 2 neighbouring dimensions a lane (the binary digits of 2 * kDb).
-template <int kDb>
-struct Pieces {
-  static constexpr int kN = (kDb >> 3) + ((kDb >> 2) & 1) + ((kDb >> 1) & 1) + (kDb & 1);
-  static constexpr int width(int c) {
-    for (int w = 16; w >= 2; w /= 2)
-      if (2 * kDb & w)
-        if (c-- == 0) return w;
-    return 0;
-  }
-  static constexpr int base(int c) { return c == 0 ? 0 : base(c - 1) + 16 * width(c - 1); }
-};
-
-template <int kN, typename F, int... kI>
-__device__ __forceinline__ void each_piece(F &&f, std::integer_sequence<int, kI...>) {
-  (f(std::integral_constant<int, kI>{}), ...);
-}
-template <int kN, typename F>
-__device__ __forceinline__ void each_piece(F &&f) {
-  each_piece<kN>(f, std::make_integer_sequence<int, kN>{});
-}
-
-template <int kBytes>
-__device__ __forceinline__ void load_bytes(uint32_t *dst, const uint8_t *src) {
-  if constexpr (kBytes >= 16) {
-#pragma unroll
-    for (int i = 0; i < kBytes / 16; ++i) {
-      const u32x4 v = reinterpret_cast<const u32x4 *>(src)[i];
-      dst[4 * i] = v[0], dst[4 * i + 1] = v[1], dst[4 * i + 2] = v[2], dst[4 * i + 3] = v[3];
-    }
-  } else if constexpr (kBytes == 8) {
-    const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
-    dst[0] = v[0], dst[1] = v[1];
-  } else if constexpr (kBytes == 4) {
-    dst[0] = *reinterpret_cast<const uint32_t *>(src);
-  } else {
-    dst[0] = *reinterpret_cast<const uint16_t *>(src);
-  }
-}
-
-// Two e4m3fn codes times 2^e as a bf16 pair (exact: 4 bits of significand).
-__device__ __forceinline__ uint32_t mx_pair(uint32_t codes, float scale, bool high) {
-  return __builtin_bit_cast(
-      uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(int(codes), scale, true)
-                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(int(codes), scale, false));
-}
-
-__device__ __forceinline__ bf16x8 as_frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
-}
-
-// Over the 4 lanes of one column (l, l ^ 16, l ^ 32, l ^ 48).
-__device__ __forceinline__ float column_max(float x) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float column_sum(float x) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // The places of a sequence that are seen, from its start rounded down to a tile.
 struct Seen {
   int start, len, base, units;
@@ -182,16 +114,6 @@ __device__ __forceinline__ Seen seen_of(const PagedAttention &a, int64_t s) {
   const int base = start / kTile * kTile;
   return {start, len, base, int((int64_t(len) - base + kUnit - 1) / kUnit)};
 }
-
-// 32 places' keys and values in a lane's registers, as they lie in the cache.
-template <int kDb, bool kMx>
-struct Held {
-  static constexpr int kN = Pieces<kDb>::kN;
-  uint32_t k[2][kMx ? 2 * kDb : 4 * kDb];      // place l % 16 of either tile
-  uint32_t ks[2][(kDb + 1) / 2];
-  uint32_t v[8][kMx ? (kDb + 1) / 2 : kDb];    // places 4 g .. 4 g + 3 of either tile
-  uint32_t vs[8][kN];
-};
 
 // Where a run starts: this workgroup's first unit is unit `local` of the
 // sequence s's pairs.  Writes the workspace's `before` too (workgroup 0).

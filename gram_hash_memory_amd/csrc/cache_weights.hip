@@ -2,7 +2,7 @@
 //
 //   w_p += sum over the tokens and heads that see p of e^(z_p - lse),
 //
-// with z as in chunk_attention.hip.  A wave owns 32 places of one key-value head:
+// with z as in tile_wide.hip.  A wave owns 32 places of one key-value head:
 // their keys stay in its registers as matrix-core operands, the query rows of the
 // sequence go by 32 at a time, and a lane adds up the weights of 8 places from
 // every 16th row, in row order; lanes are joined once, at the end.  One wave writes

@@ -210,7 +210,7 @@ struct AttentionRules {
   float cap;
 };
 
-// Attention of several query rows a key-value head (chunk_attention.hip).  With
+// Attention of several query rows a key-value head (tile_plan.hip).  With
 // prefix_table the sequences have one new token each, cu cuts them into groups,
 // and a group shares the prefix_lens[g] places of row g of prefix_table; else cu
 // cuts the T tokens into sequences.

@@ -1,0 +1,378 @@
+// The plan of attention of several query rows a key-value head, and the join of its
+// parts.
+//
+// The host knows neither the tokens of a sequence nor its length, so a kernel of one
+// workgroup a list writes the blocks down.  Where there are enough blocks, the
+// workgroups of the lists' kernels take whole ones off a queue; where there are too
+// few to fill the GPU, equal runs of all tiles, and a third kernel adds the parts of
+// a block in order.
+#include <algorithm>
+
+#include "attention_common.hpp"
+#include "tile_plan.hpp"
+
+namespace engram {
+namespace {
+
+using namespace attn;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kWholePlaces = 512;          // contexts that are never cut
+constexpr int kJoinTiles = 4;              // what cutting costs, in tiles
+
+inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
+
+// The sum of x over the threads before this one; *total: over all of them.
+__device__ __forceinline__ int scan_before(int x, int *total) {
+  __shared__ int wave_lds[kPlanThreads / 64];
+  int upto = x;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int y = __shfl_up(upto, d);
+    if (int(threadIdx.x & 63) >= d) upto += y;
+  }
+  __syncthreads();                           // wave_lds may still be read
+  if ((threadIdx.x & 63) == 63) wave_lds[threadIdx.x >> 6] = upto;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    if (w == int(threadIdx.x >> 6)) upto += sum;
+    sum += wave_lds[w];
+  }
+  *total = sum;
+  return upto - x;
+}
+
+__device__ __forceinline__ int max_all(int x) {
+  __shared__ int wave_lds[kPlanThreads / 64];
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x = max(x, __shfl_xor(x, d));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) wave_lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = wave_lds[0];
+#pragma unroll
+  for (int w = 1; w < kPlanThreads / 64; ++w) x = max(x, wave_lds[w]);
+  return x;
+}
+
+// The new tokens of problem i: a chunk's sequences, or the groups and then the
+// sequences over their own places.
+__device__ __forceinline__ int tokens_of(const TileAttention &a, int i, int *token0) {
+  if (a.prefix_table && i >= a.n_groups) {
+    *token0 = i - a.n_groups;
+    return 1;
+  }
+  const int begin = min(max(a.cu[i], 0), a.T), end = min(max(a.cu[i + 1], begin), a.T);
+  *token0 = begin;
+  return end - begin;
+}
+
+// Which list problem i belongs to.
+__device__ __forceinline__ int list_of(const TileAttention &a, const TilePlan &plan, int i, int rows) {
+  return (a.prefix_table && i >= a.n_groups) || rows <= plan.narrow_rows ? 1 : 0;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, TilePlan plan) {
+  const TileList list = plan.list[blockIdx.x];
+  if (list.max_blocks == 0) return;
+  const int group = a.q_heads / a.cache.kv_heads, tid = threadIdx.x;
+  const int problems = a.n_groups + a.n_seqs;
+  int blocks = 0;
+  for (int base = 0; base < problems; base += kPlanThreads) {
+    const int i = base + tid;
+    int token0, n = 0;
+    if (i < problems) {
+      const int rows = tokens_of(a, i, &token0) * group;
+      if (list_of(a, plan, i, rows) == int(blockIdx.x)) n = (rows + list.block_rows - 1) / list.block_rows;
+    }
+    int total;
+    const int at = blocks + scan_before(n, &total);
+    blocks += total;
+    if (i < problems) list.first_block[i] = at;
+    for (int k = 0; k < n && at + k < list.max_blocks; ++k) {
+      list.blocks[at + k].seq = i;
+      list.blocks[at + k].row0 = k * list.block_rows;
+    }
+  }
+  blocks = min(blocks, list.max_blocks);     // more only where cu does not rise
+  __syncthreads();
+
+  int units = 0, longest = 0;
+  for (int base = 0; base < blocks; base += kPlanThreads) {
+    const int b = base + tid;
+    int mine = 0;
+    TileBlock w{};
+    if (b < blocks) {
+      const int i = list.blocks[b].seq;
+      w.row0 = list.blocks[b].row0;
+      const int n = tokens_of(a, i, &w.token0);
+      w.rows = min(list.block_rows, n * group - w.row0);
+      w.group = -1;
+      if (!a.prefix_table) {
+        w.kind = kChunk, w.seq = i;
+        w.len = length_of(a.lens[i], a.max_len, a.table_width, a.cache.page_shift);
+        w.first = w.len - n;
+        const int t0 = w.row0 / group, t1 = (w.row0 + w.rows - 1) / group;
+        int a_lo = 0x7FFFFFFF, a_hi = 0, b_lo = 0x7FFFFFFF, b_hi = 0;
+        auto add = [&](int t) {
+          const RowSees r = row_sees(a.rules, i, w.token0 + t, w.first + t, w.len);
+          if (r.n > 0) b_lo = min(b_lo, r.lo), b_hi = max(b_hi, r.lo + r.n);
+          if (r.m > 0) a_lo = min(a_lo, r.first), a_hi = max(a_hi, r.first + r.m);
+        };
+        if (a.rules.doc_starts) {
+#pragma unroll 8
+          for (int t = t0; t <= t1; ++t) add(t);
+        } else {                             // the first token sees the first place, the last one the last
+          add(t0);
+          add(t1);
+        }
+        if (a_hi > 0) w.a_lo = a_lo, w.a_hi = a_hi;
+        if (b_hi > 0) w.b_lo = b_lo, w.b_hi = b_hi;
+      } else if (i < a.n_groups) {
+        w.kind = kSharedPrefix, w.seq = i;
+        w.len = length_of(a.prefix_lens[i], a.max_prefix, a.prefix_width, a.cache.page_shift);
+        w.b_hi = w.len;
+      } else {
+        w.kind = kOwnPlaces, w.seq = i - a.n_groups;
+        w.len = length_of(a.lens[w.seq], a.max_len, a.table_width, a.cache.page_shift);
+        w.b_hi = w.len;
+        // The last group that does not begin behind the sequence.
+        int lo = 0, hi = a.n_groups;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (a.cu[mid] <= w.seq) lo = mid + 1;
+          else hi = mid;
+        }
+        if (lo > 0) {
+          int begin;
+          const int members = tokens_of(a, lo - 1, &begin);
+          if (w.seq >= begin && w.seq < begin + members) {
+            w.group = lo - 1;
+            w.group_row = (w.seq - begin) * group + w.row0;
+          }
+        }
+      }
+      w.a_tile = w.a_lo / list.tile;
+      w.a_n = w.a_hi > 0 ? (w.a_hi - 1) / list.tile + 1 - w.a_tile : 0;
+      w.b_tile = w.b_lo / list.tile;
+      if (w.a_n > 0) w.b_tile = max(w.b_tile, w.a_tile + w.a_n);
+      w.b_n = w.b_hi > 0 ? max(0, (w.b_hi - 1) / list.tile + 1 - w.b_tile) : 0;
+      // A chunk's rows that see nothing need their zeros: a tile without places.
+      if (w.kind == kChunk && w.tiles() == 0) w.b_n = 1;
+      mine = w.tiles();
+      longest = max(longest, mine);
+    }
+    int total;
+    w.before = units + scan_before(mine, &total);
+    units += total;
+    if (b < blocks) list.blocks[b] = w;
+  }
+  longest = max_all(longest);
+  if (tid == 0) {
+    // Whole blocks off a queue take as long as their mean load and half a block, or
+    // as the longest one; runs as long as their share, and the join of its parts.
+    const int64_t pairs = int64_t(blocks) * a.cache.kv_heads;
+    const int64_t total = int64_t(units) * a.cache.kv_heads;
+    const int per = int(max(int64_t(1), (total + list.runs - 1) / list.runs));
+    const int64_t queued = max(int64_t(longest), pairs > list.runs ? per + longest / 2 : 0);
+    *list.header = TileHeader{units, blocks, per, !list.can_split || queued <= per + kJoinTiles};
+    *list.queue = 0;
+  }
+}
+
+// ---------------------------------------------------------------- the join
+
+// The blocks' rows, D / 4 lanes each, chunks workgroups a (block, head): a row's
+// parts to its result, in order.  A chunk's rows, or those of the own places, which
+// look up their group's.
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void tile_join_kernel(TileAttention a, TilePlan plan, int which, int chunks) {
+  const TileList &list = plan.list[which];
+  const TileHeader head = *list.header;
+  const int D = a.cache.head_dim, lanes = D / 4, at_once = kJoinThreads / lanes;
+  const int b = blockIdx.x / (a.cache.kv_heads * chunks);
+  const int rest = blockIdx.x % (a.cache.kv_heads * chunks), kvh = rest / chunks;
+  if (b >= head.blocks) return;
+  const bool both = plan.whole_rows > 0;
+  if (!both && head.direct) return;
+  const TileBlock w = list.blocks[b];
+  const int slot = threadIdx.x / lanes, at = threadIdx.x % lanes;
+  if (slot >= at_once || w.kind == kSharedPrefix) return;
+
+  // Where the parts of a block's row are: `n` of them from run r0 on, the first one
+  // as the run's later piece or not; or n = 1 and a row of whole pieces.
+  struct Parts {
+    int64_t place;
+    int n, r0, later;
+  };
+  auto parts_of = [&](const TileList &l, const TileHeader &h, const TileBlock &x, int64_t q_row) {
+    Parts p{0, 0, 0, 0};
+    if (x.tiles() == 0) return p;
+    p.place = (x.kind == kSharedPrefix ? int64_t(a.T) * a.q_heads : 0) + q_row;
+    p.n = 1, p.r0 = -1;
+    if (h.direct) return p;
+    const int64_t u0 = int64_t(kvh) * h.units + x.before;
+    const int r0 = int(u0 / h.per), r1 = int((u0 + x.tiles() - 1) / h.per);
+    if (r0 != r1) p.n = r1 - r0 + 1, p.r0 = r0, p.later = int64_t(r0) * h.per < u0;
+    return p;
+  };
+
+  for (int row = rest % chunks * at_once + slot; row < w.rows; row += chunks * at_once) {
+    const int64_t q_row = query_row(a, w, kvh, row).at;
+    const Parts mine = parts_of(list, head, w, q_row);
+    if (!both && mine.n == 1) return;        // written already: so is the whole block
+    Parts prefix{0, 0, 0, 0};
+    const TileList *from = nullptr;
+    int prefix_row = 0;
+    if (both && w.group >= 0) {
+      int begin;
+      const int rows = tokens_of(a, w.group, &begin) * (a.q_heads / a.cache.kv_heads);
+      from = &plan.list[list_of(a, plan, w.group, rows)];
+      const int in_group = w.group_row + row;
+      prefix_row = in_group % from->block_rows;
+      prefix = parts_of(*from, *from->header, from->blocks[from->first_block[w.group] + in_group / from->block_rows], q_row);
+    }
+    auto place_of = [&](int i) {
+      if (i < prefix.n) return prefix.r0 < 0 ? prefix.place : from->part_row(prefix.r0 + i, i == 0 && prefix.later, prefix_row);
+      i -= prefix.n;
+      return mine.r0 < 0 ? mine.place : list.part_row(mine.r0 + i, i == 0 && mine.later, row);
+    };
+    const int n = prefix.n + mine.n;
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) top = fmaxf(top, plan.ml[place_of(i)].x);
+    const float ms = top == -INFINITY ? 0.0f : top;
+    f32x4 o{};
+    float l = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const int64_t place = place_of(i);
+      const float2 ml = plan.ml[place];
+      const f32x4 v = reinterpret_cast<const f32x4 *>(plan.o)[place * lanes + at];
+      const float keep = __builtin_amdgcn_exp2f(ml.x - ms);
+      o += v * keep;
+      l += ml.y * keep;
+    }
+    if (at == 0 && a.lse) a.lse[q_row] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    reinterpret_cast<u32x2 *>(a.out + q_row * D)[at] =
+        u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+  }
+}
+
+// ---------------------------------------------------------------- the sizes
+
+struct Sizes {
+  TileList list[2];
+  int64_t whole_rows, rows;                  // rows: of parts, all together
+  int32_t narrow_rows;
+};
+
+Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+               int32_t max_len, int32_t max_prefix) {
+  Sizes s{};
+  const int64_t group = q_heads / kv_heads, rows = T * group;
+  const int64_t problems = n_groups > 0 ? n_groups : n_seqs;
+  TileList &wide = s.list[0], &narrow = s.list[1];
+  // Few rows a problem on the average: all of them in narrow blocks.  Else narrow
+  // blocks for the problems that have no more than one, where there may be some
+  // whose places take long to read.
+  const bool all_narrow = rows <= 2 * kRows * problems;
+  const bool some_narrow = all_narrow || n_groups > 0 || (n_seqs > 1 && max_len > 2 * kWholePlaces);
+  s.narrow_rows = all_narrow ? 0x7FFFFFFF : some_narrow ? kRows : 0;
+  narrow.block_rows = kRows;
+  narrow.tile = kNarrowTile;
+  narrow.runs = 512;
+  // 8 waves where a problem has the rows for them and the registers suffice.
+  const int waves = head_dim <= 128 && rows > 4 * kRows * problems ? 8 : 4;
+  wide.block_rows = kRows * waves;
+  wide.tile = kWideTile;
+  wide.runs = waves == 8 || head_dim > 128 ? 256 : 512;
+  if (!all_narrow) wide.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, rows / wide.block_rows + problems));
+  if (some_narrow) {
+    const int64_t most = all_narrow ? rows / kRows + problems : problems;
+    narrow.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, most + (n_groups > 0 ? n_seqs * ceil_div(group, kRows) : 0)));
+  }
+  s.whole_rows = n_groups > 0 ? 2 * int64_t(T) * q_heads : 0;
+  s.rows = s.whole_rows;
+  for (TileList &l : s.list) {
+    l.can_split = std::max(max_len, max_prefix) > kWholePlaces;
+    l.parts = s.rows;
+    if (l.can_split && l.max_blocks > 0) s.rows += 2 * int64_t(l.runs) * l.block_rows;
+  }
+  return s;
+}
+
+inline int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Lays the plan out from `base` on; returns its bytes.
+int64_t lay_out(const Sizes &s, int64_t problems, int64_t head_dim, uint8_t *base, TilePlan *plan) {
+  int64_t at = 256;
+  for (int i = 0; i < 2; ++i) {
+    TileList l = s.list[i];
+    l.header = reinterpret_cast<TileHeader *>(base + 128 * i);
+    l.queue = reinterpret_cast<int32_t *>(base + 128 * i + 64);
+    l.blocks = reinterpret_cast<TileBlock *>(base + at);
+    at += align256(l.max_blocks * int64_t(sizeof(TileBlock)));
+    l.first_block = reinterpret_cast<int32_t *>(base + at);
+    if (l.max_blocks > 0) at += align256(problems * 4);
+    plan->list[i] = l;
+  }
+  plan->ml = reinterpret_cast<float2 *>(base + at);
+  at += align256(s.rows * int64_t(sizeof(float2)));
+  plan->o = reinterpret_cast<float *>(base + at);
+  plan->whole_rows = s.whole_rows;
+  plan->narrow_rows = s.narrow_rows;
+  return at + s.rows * head_dim * int64_t(sizeof(float));
+}
+
+// Workgroups of a (block, head) in the join: one for each run of rows that it takes at once.
+int join_chunks(const TileAttention &a, int block_rows) {
+  const int group = a.q_heads / a.cache.kv_heads, at_once = kJoinThreads / (a.cache.head_dim / 4);
+  const int64_t rows = std::min<int64_t>(block_rows, (a.n_groups > 0 ? 1 : int64_t(a.T)) * group);
+  return int(ceil_div(rows, at_once));
+}
+
+constexpr int64_t kMostGroups = (int64_t(1) << 32) / kJoinThreads - 1;
+
+}  // namespace
+
+int64_t tile_attention_workspace(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t max_len, int32_t max_prefix) {
+  const Sizes s = sizes_of(T, n_seqs, n_groups, q_heads, kv_heads, head_dim, max_len, max_prefix);
+  const int64_t tiles = ceil_div(std::max(max_len, max_prefix), kWideTile) + 2;
+  const int64_t rows = int64_t(T) * (q_heads / kv_heads);
+  if (rows > 1 << 30 || s.whole_rows > 0x7FFFFFFF) return -1;
+  for (const TileList &l : s.list) {
+    // Tiles are counted in 31 bits, a head's and a run's; the join's workgroups in 24.
+    if (l.max_blocks > 0x7FFFFFFF / tiles / kv_heads) return -1;
+    if ((l.can_split || s.whole_rows > 0) && int64_t(l.max_blocks) * kv_heads * l.block_rows > kMostGroups) return -1;
+  }
+  TilePlan plan;
+  return lay_out(s, n_groups + int64_t(n_seqs), head_dim, nullptr, &plan);
+}
+
+hipError_t launch_tile_attention(const TileAttention &a, hipStream_t stream) {
+  const int D = a.cache.head_dim, hkv = a.cache.kv_heads;
+  const Sizes s = sizes_of(a.T, a.n_seqs, a.n_groups, a.q_heads, hkv, D, a.max_len, a.max_prefix);
+  TilePlan plan{};
+  lay_out(s, a.n_groups + int64_t(a.n_seqs), D, static_cast<uint8_t *>(a.workspace), &plan);
+  hipLaunchKernelGGL(plan_kernel, dim3(2), dim3(kPlanThreads), 0, stream, a, plan);
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && plan.list[0].max_blocks > 0) err = launch_tile_wide(a, plan, stream);
+  if (err == hipSuccess && plan.list[1].max_blocks > 0) err = launch_tile_narrow(a, plan, stream);
+  for (int i = 0; i < 2 && err == hipSuccess; ++i) {
+    const TileList &l = plan.list[i];
+    if (l.max_blocks == 0 || !(l.can_split || plan.whole_rows > 0)) continue;
+    if (plan.whole_rows > 0 && i == 0) continue;      // the own places are in the narrow list
+    const int chunks = join_chunks(a, l.block_rows);
+    hipLaunchKernelGGL(tile_join_kernel, dim3(unsigned(int64_t(l.max_blocks) * hkv * chunks)), dim3(kJoinThreads), 0, stream,
+                       a, plan, i, chunks);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+}  // namespace engram

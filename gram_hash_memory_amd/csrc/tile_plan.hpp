@@ -1,5 +1,13 @@
-// What the tile kernels of chunk_attention.hip work at: blocks of query rows, the
-// tiles of places that each block sees, and where parts of results are kept.
+// How attention of several query rows a key-value head is cut up (tile_plan.hip),
+// for the kernels that compute it (tile_wide.hip, tile_narrow.hip).
+//
+// A problem is a sequence's new tokens over its places, a group of sequences over
+// their prefix, or a sequence's one token over its own places.  Its query rows of
+// one key-value head (token-major, the heads of its group inside) are cut into
+// blocks, and the places that a block's rows see into tiles.  Problems of many rows
+// go to the wide list, whose blocks have 128 or 256 rows, one of 32 a wave: bound
+// by the matrix cores.  Problems of few go to the narrow list, whose blocks have 32
+// rows and whose waves share the places: bound by reading them.
 #pragma once
 
 #include "common.hpp"
@@ -7,15 +15,16 @@
 namespace engram {
 namespace attn {
 
-constexpr int kTile = 64;                  // places of a tile
+constexpr int kRows = 32;                  // query rows of a wave
+constexpr int kWideTile = 64;              // places of a tile
+constexpr int kNarrowWaves = 4, kNarrowTile = 32 * kNarrowWaves;
 
 enum TileKind : int32_t { kChunk = 0, kSharedPrefix = 1, kOwnPlaces = 2 };
 
-// A block of query rows of one problem (a sequence's new tokens, a group's
-// sequences over their prefix, a sequence over its own places), for every
-// key-value head: rows row0 .. row0 + rows - 1 of the problem, row = token * group
-// + head of the group.  Its rows see places of [a_lo, a_hi) and [b_lo, b_hi); its
-// tiles are a_n from a_tile on, then b_n from b_tile on, none of them twice.
+// A block of query rows, for every key-value head: rows row0 .. row0 + rows - 1 of
+// its problem, row = token * group + head of the group.  Its rows see places of
+// [a_lo, a_hi) and [b_lo, b_hi); its tiles are a_n from a_tile on, then b_n from
+// b_tile on, none of them twice.
 struct TileBlock {
   int32_t kind, seq;                       // seq: the row of the page table
   int32_t token0, first;                   // the problem's first token, and its place
@@ -23,7 +32,17 @@ struct TileBlock {
   int32_t a_lo, a_hi, b_lo, b_hi;
   int32_t a_tile, a_n, b_tile, b_n;
   int32_t before;                          // tiles of a head in the blocks before this one
-  int32_t prefix_block, prefix_row;        // own places: the group's first block, the first row in it (-1: none)
+  int32_t group, group_row;                // own places: the group (-1: none), the first row in it
+
+  __device__ __forceinline__ int tiles() const { return a_n + b_n; }
+  // The first place of tile t of `size` places.
+  __device__ __forceinline__ int place(int t, int size) const {
+    return (t < a_n ? a_tile + t : b_tile + t - a_n) * size;
+  }
+  // Whether any row sees place p.
+  __device__ __forceinline__ bool used(int p) const {
+    return unsigned(p - b_lo) < unsigned(b_hi - b_lo) || unsigned(p - a_lo) < unsigned(a_hi - a_lo);
+  }
 };
 
 struct TileHeader {
@@ -33,22 +52,32 @@ struct TileHeader {
   int32_t direct;                          // whole blocks off the queue instead of runs
 };
 
-// The workspace.  o and ml hold rows of results before their division by the sum:
-// first a row for each query row of whole pieces (shared prefix: two, for the
-// prefix and the own places), then two blocks for each run.
-struct TilePlan {
+// One list of blocks, in the workspace.
+struct TileList {
   TileHeader *header;
   int32_t *queue;
   TileBlock *blocks;
-  int32_t *first_block;                    // of each problem
+  int32_t *first_block;                    // of each problem of the list
+  int32_t max_blocks, runs;                // workgroups
+  int32_t block_rows, tile;
+  int32_t can_split;
+  int64_t parts;                           // where its runs' parts begin in o and ml
+
+  // A run's first piece, or a later one (its last), of a block that it does not hold whole.
+  __device__ __forceinline__ int64_t part_row(int run, bool later, int row) const {
+    return parts + (2 * int64_t(run) + later) * block_rows + row;
+  }
+};
+
+// o and ml hold rows of results before their division by the sum: with a shared
+// prefix first one for each query row of whole pieces over the own places, then one
+// of those over the prefix; then two blocks for each run.
+struct TilePlan {
+  TileList list[2];                        // wide, narrow
   float *o;
   float2 *ml;
-  int32_t max_blocks, runs, whole_rows;
-  int32_t can_split;
-
-  __device__ __forceinline__ int64_t part_row(int run, bool later, int block, int row) const {
-    return whole_rows + (2 * int64_t(run) + later) * block + row;
-  }
+  int64_t whole_rows;                      // 0: whole pieces are results
+  int32_t narrow_rows;                     // most rows of a narrow problem (own places are always narrow)
 };
 
 // What a query row sees: places lo .. lo + n - 1 and first .. first + m - 1.
@@ -74,5 +103,81 @@ __device__ __forceinline__ int length_of(int stated, int max_len, int width, int
   return int(min(int64_t(min(max(stated, 0), max_len)), int64_t(width) << page_shift));
 }
 
+// A query row of a block, of one key-value head.
+struct QueryRow {
+  int tok, token, head;
+  int64_t at;                              // in q, out and lse, in rows
+};
+__device__ __forceinline__ QueryRow query_row(const TileAttention &a, const TileBlock &w, int kvh, int row) {
+  const int group = a.q_heads / a.cache.kv_heads, in_problem = w.row0 + row;
+  QueryRow q;
+  q.tok = in_problem / group;
+  q.token = w.token0 + q.tok;
+  q.head = kvh * group + in_problem - q.tok * group;
+  q.at = int64_t(q.token) * a.q_heads + q.head;
+  return q;
+}
+
+// Scores are kept in units of log 2: z = unit * (q.k), the sign of the scale in q
+// (q is zeroed where the scale is 0); with a cap, cap2 * tanh(z).
+struct ScoreUnit {
+  float unit, cap2;
+  uint32_t flip, keep;
+};
+__device__ __forceinline__ ScoreUnit score_unit(const TileAttention &a, float log2e) {
+  const float s = fabsf(a.scale);
+  ScoreUnit u;
+  u.unit = s == 0.0f ? 1.0f : a.rules.cap > 0.0f ? s / a.rules.cap : s * log2e;
+  u.cap2 = a.rules.cap * log2e;
+  u.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  u.keep = s == 0.0f ? 0u : 0xFFFFFFFFu;
+  return u;
+}
+
+// The block and tile that a workgroup begins with, and the tiles of its run.  All
+// threads; false: nothing to do.
+struct Work {
+  int run, left, block, unit, kvh;
+};
+__device__ __forceinline__ bool first_work(const TileList &list, const TileHeader &head, int kv_heads, int threads,
+                                           int *lds, Work *w) {
+  *w = Work{int(blockIdx.x), 0, 0, 0, 0};
+  if (head.direct) return head.blocks > 0;
+  // Neighbouring runs share keys: they go to one XCD.
+  if (list.runs % 8 == 0) w->run = w->run % 8 * (list.runs / 8) + w->run / 8;
+  const int64_t total = int64_t(head.units) * kv_heads, u0 = int64_t(w->run) * head.per;
+  if (u0 >= total) return false;
+  w->left = int(min(int64_t(head.per), total - u0));
+  w->kvh = int(u0 / head.units);
+  const int local = int(u0 - int64_t(w->kvh) * head.units);
+  for (int b = threadIdx.x; b < head.blocks; b += threads) {
+    const int at = local - list.blocks[b].before;
+    if (at >= 0 && at < list.blocks[b].tiles()) lds[0] = b, lds[1] = at;
+  }
+  __syncthreads();
+  w->block = __builtin_amdgcn_readfirstlane(lds[0]);
+  w->unit = __builtin_amdgcn_readfirstlane(lds[1]);
+  __syncthreads();
+  return true;
+}
+// The next whole block off the queue; false: none is left.
+__device__ __forceinline__ bool next_block(const TileList &list, const TileHeader &head, int kv_heads, int *lds,
+                                           Work *w) {
+  if (threadIdx.x == 0) lds[0] = atomicAdd(list.queue, 1);
+  __syncthreads();
+  const int at = __builtin_amdgcn_readfirstlane(lds[0]);
+  __syncthreads();
+  if (at >= head.blocks * kv_heads) return false;
+  w->block = head.blocks - 1 - at / kv_heads;        // a sequence's last blocks see most
+  w->kvh = at % kv_heads;
+  w->unit = 0;
+  return true;
+}
+
 }  // namespace attn
+
+// tile_wide.hip, tile_narrow.hip: plan.list[0] and plan.list[1].
+hipError_t launch_tile_wide(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
+hipError_t launch_tile_narrow(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
+
 }  // namespace engram
