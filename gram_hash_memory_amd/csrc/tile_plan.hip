@@ -18,7 +18,7 @@ using namespace attn;
 
 constexpr int kPlanThreads = 1024;
 constexpr int kWholePlaces = 512;          // contexts that are never cut
-constexpr int kJoinTiles = 4;              // what cutting costs, in tiles
+constexpr int kJoinTiles[2] = {6, 3};      // what cutting costs, in tiles of a list
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -75,7 +75,7 @@ __device__ __forceinline__ int list_of(const TileAttention &a, const TilePlan &p
 }
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, TilePlan plan) {
-  const TileList list = plan.list[blockIdx.x];
+  const TileList list = blockIdx.x == 0 ? plan.list[0] : plan.list[1];
   if (list.max_blocks == 0) return;
   const int group = a.q_heads / a.cache.kv_heads, tid = threadIdx.x;
   const int problems = a.n_groups + a.n_seqs;
@@ -177,80 +177,95 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
     const int64_t total = int64_t(units) * a.cache.kv_heads;
     const int per = int(max(int64_t(1), (total + list.runs - 1) / list.runs));
     const int64_t queued = max(int64_t(longest), pairs > list.runs ? per + longest / 2 : 0);
-    *list.header = TileHeader{units, blocks, per, !list.can_split || queued <= per + kJoinTiles};
+    *list.header = TileHeader{units, blocks, per, !list.can_split || queued <= per + kJoinTiles[blockIdx.x]};
     *list.queue = 0;
   }
 }
 
 // ---------------------------------------------------------------- the join
 
-// The blocks' rows, D / 4 lanes each, chunks workgroups a (block, head): a row's
-// parts to its result, in order.  A chunk's rows, or those of the own places, which
-// look up their group's.
+// A row's parts to its result, in order; D / 4 lanes a row, `chunks` workgroups a
+// (block, head).  Without a shared prefix the blocks of `list` that runs cut, one for
+// the first boundary in each; with one all blocks of own places (the narrow list),
+// whose rows look up their group's.
 constexpr int kJoinThreads = 256;
-__global__ __launch_bounds__(kJoinThreads) void tile_join_kernel(TileAttention a, TilePlan plan, int which, int chunks) {
-  const TileList &list = plan.list[which];
+__global__ __launch_bounds__(kJoinThreads) void tile_join_kernel(TileAttention a, TilePlan plan, TileList list, int chunks,
+                                                                 bool both) {
+  __shared__ int found_lds;
   const TileHeader head = *list.header;
-  const int D = a.cache.head_dim, lanes = D / 4, at_once = kJoinThreads / lanes;
-  const int b = blockIdx.x / (a.cache.kv_heads * chunks);
-  const int rest = blockIdx.x % (a.cache.kv_heads * chunks), kvh = rest / chunks;
-  if (b >= head.blocks) return;
-  const bool both = plan.whole_rows > 0;
-  if (!both && head.direct) return;
+  const int D = a.cache.head_dim, lanes = D / 4, at_once = kJoinThreads / lanes, kv_heads = a.cache.kv_heads;
+  const int chunk = blockIdx.x % chunks;
+  int b = blockIdx.x / chunks, kvh;
+  if (both) {
+    kvh = b % kv_heads, b /= kv_heads;
+    if (b >= head.blocks) return;
+  } else {
+    // The block that run b + 1 cuts, unless an earlier run does.
+    if (head.direct) return;
+    const int64_t total = int64_t(head.units) * kv_heads, u = int64_t(b + 1) * head.per;
+    if (u >= total) return;
+    kvh = int(u / head.units);
+    const int local = int(u - int64_t(kvh) * head.units);
+    if (threadIdx.x == 0) found_lds = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < head.blocks; i += kJoinThreads) {
+      const int at = local - list.blocks[i].before;
+      if (at > 0 && at < list.blocks[i].tiles() && at <= head.per) found_lds = i;
+    }
+    __syncthreads();
+    b = found_lds;
+    if (b < 0) return;
+  }
   const TileBlock w = list.blocks[b];
   const int slot = threadIdx.x / lanes, at = threadIdx.x % lanes;
   if (slot >= at_once || w.kind == kSharedPrefix) return;
 
-  // Where the parts of a block's row are: `n` of them from run r0 on, the first one
-  // as the run's later piece or not; or n = 1 and a row of whole pieces.
+  // Where the parts of a block's row are: n of them from run r0 on, the first one the
+  // run's later piece or not; or one, a row of whole pieces (r0 < 0).
   struct Parts {
-    int64_t place;
-    int n, r0, later;
+    int64_t place;                           // of the whole row, or of the first run's part
+    int n, stride;
+    bool later;
   };
-  auto parts_of = [&](const TileList &l, const TileHeader &h, const TileBlock &x, int64_t q_row) {
-    Parts p{0, 0, 0, 0};
-    if (x.tiles() == 0) return p;
-    p.place = (x.kind == kSharedPrefix ? int64_t(a.T) * a.q_heads : 0) + q_row;
-    p.n = 1, p.r0 = -1;
-    if (h.direct) return p;
+  auto parts_of = [&](const TileHeader &h, const TileBlock &x, int64_t parts, int block_rows, int64_t q_row, int row) {
+    Parts p{(x.kind == kSharedPrefix ? int64_t(a.T) * a.q_heads : 0) + q_row, x.tiles() > 0 ? 1 : 0, 0, false};
+    if (h.direct || x.tiles() == 0) return p;
     const int64_t u0 = int64_t(kvh) * h.units + x.before;
     const int r0 = int(u0 / h.per), r1 = int((u0 + x.tiles() - 1) / h.per);
-    if (r0 != r1) p.n = r1 - r0 + 1, p.r0 = r0, p.later = int64_t(r0) * h.per < u0;
+    if (r0 != r1) p = Parts{parts + 2 * int64_t(r0) * block_rows + row, r1 - r0 + 1, block_rows, int64_t(r0) * h.per < u0};
     return p;
   };
+  auto place_of = [](const Parts &p, int i) { return p.place + (2 * int64_t(i) + (i == 0 && p.later)) * p.stride; };
 
-  for (int row = rest % chunks * at_once + slot; row < w.rows; row += chunks * at_once) {
+  for (int row = chunk * at_once + slot; row < w.rows; row += chunks * at_once) {
     const int64_t q_row = query_row(a, w, kvh, row).at;
-    const Parts mine = parts_of(list, head, w, q_row);
-    if (!both && mine.n == 1) return;        // written already: so is the whole block
-    Parts prefix{0, 0, 0, 0};
-    const TileList *from = nullptr;
-    int prefix_row = 0;
+    const Parts mine = parts_of(head, w, list.parts, list.block_rows, q_row, row);
+    Parts prefix{0, 0, 0, false};
     if (both && w.group >= 0) {
       int begin;
-      const int rows = tokens_of(a, w.group, &begin) * (a.q_heads / a.cache.kv_heads);
-      from = &plan.list[list_of(a, plan, w.group, rows)];
+      const int rows = tokens_of(a, w.group, &begin) * (a.q_heads / kv_heads);
+      const bool narrow = list_of(a, plan, w.group, rows) == 1;
+      const int64_t parts = narrow ? plan.list[1].parts : plan.list[0].parts;
+      const int block_rows = narrow ? plan.list[1].block_rows : plan.list[0].block_rows;
+      const TileBlock *blocks = narrow ? plan.list[1].blocks : plan.list[0].blocks;
+      const int32_t *first = narrow ? plan.list[1].first_block : plan.list[0].first_block;
+      const TileHeader h = narrow ? *plan.list[1].header : *plan.list[0].header;
       const int in_group = w.group_row + row;
-      prefix_row = in_group % from->block_rows;
-      prefix = parts_of(*from, *from->header, from->blocks[from->first_block[w.group] + in_group / from->block_rows], q_row);
+      prefix = parts_of(h, blocks[first[w.group] + in_group / block_rows], parts, block_rows, q_row, in_group % block_rows);
     }
-    auto place_of = [&](int i) {
-      if (i < prefix.n) return prefix.r0 < 0 ? prefix.place : from->part_row(prefix.r0 + i, i == 0 && prefix.later, prefix_row);
-      i -= prefix.n;
-      return mine.r0 < 0 ? mine.place : list.part_row(mine.r0 + i, i == 0 && mine.later, row);
-    };
     const int n = prefix.n + mine.n;
+    auto place = [&](int i) { return i < prefix.n ? place_of(prefix, i) : place_of(mine, i - prefix.n); };
     float top = -INFINITY;
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) top = fmaxf(top, plan.ml[place_of(i)].x);
+    for (int i = 0; i < n; ++i) top = fmaxf(top, plan.ml[place(i)].x);
     const float ms = top == -INFINITY ? 0.0f : top;
     f32x4 o{};
     float l = 0.0f;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
-      const int64_t place = place_of(i);
-      const float2 ml = plan.ml[place];
-      const f32x4 v = reinterpret_cast<const f32x4 *>(plan.o)[place * lanes + at];
+      const int64_t p = place(i);
+      const float2 ml = plan.ml[p];
+      const f32x4 v = reinterpret_cast<const f32x4 *>(plan.o)[p * lanes + at];
       const float keep = __builtin_amdgcn_exp2f(ml.x - ms);
       o += v * keep;
       l += ml.y * keep;
@@ -281,10 +296,10 @@ Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int
   // whose places take long to read.
   const bool all_narrow = rows <= 2 * kRows * problems;
   const bool some_narrow = all_narrow || n_groups > 0 || (n_seqs > 1 && max_len > 2 * kWholePlaces);
-  s.narrow_rows = all_narrow ? 0x7FFFFFFF : some_narrow ? kRows : 0;
-  narrow.block_rows = kRows;
+  narrow.block_rows = tile_narrow_rows(head_dim, n_groups > 0 && !all_narrow ? group : ceil_div(rows, problems));
   narrow.tile = kNarrowTile;
-  narrow.runs = 512;
+  narrow.runs = tile_narrow_groups(head_dim, narrow.block_rows);
+  s.narrow_rows = all_narrow ? 0x7FFFFFFF : some_narrow ? narrow.block_rows : 0;
   // 8 waves where a problem has the rows for them and the registers suffice.
   const int waves = head_dim <= 128 && rows > 4 * kRows * problems ? 8 : 4;
   wide.block_rows = kRows * waves;
@@ -292,8 +307,9 @@ Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int
   wide.runs = waves == 8 || head_dim > 128 ? 256 : 512;
   if (!all_narrow) wide.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, rows / wide.block_rows + problems));
   if (some_narrow) {
-    const int64_t most = all_narrow ? rows / kRows + problems : problems;
-    narrow.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, most + (n_groups > 0 ? n_seqs * ceil_div(group, kRows) : 0)));
+    const int64_t most = all_narrow ? rows / narrow.block_rows + problems : problems;
+    const int64_t own = n_groups > 0 ? n_seqs * ceil_div(group, narrow.block_rows) : 0;
+    narrow.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, most + own));
   }
   s.whole_rows = n_groups > 0 ? 2 * int64_t(T) * q_heads : 0;
   s.rows = s.whole_rows;
@@ -328,12 +344,9 @@ int64_t lay_out(const Sizes &s, int64_t problems, int64_t head_dim, uint8_t *bas
   return at + s.rows * head_dim * int64_t(sizeof(float));
 }
 
-// Workgroups of a (block, head) in the join: one for each run of rows that it takes at once.
-int join_chunks(const TileAttention &a, int block_rows) {
-  const int group = a.q_heads / a.cache.kv_heads, at_once = kJoinThreads / (a.cache.head_dim / 4);
-  const int64_t rows = std::min<int64_t>(block_rows, (a.n_groups > 0 ? 1 : int64_t(a.T)) * group);
-  return int(ceil_div(rows, at_once));
-}
+// Workgroups of a (block, head) in the join: each takes kJoinRows rows.
+constexpr int kJoinRows = 32;
+inline int join_chunks(int block_rows) { return int(ceil_div(block_rows, kJoinRows)); }
 
 constexpr int64_t kMostGroups = (int64_t(1) << 32) / kJoinThreads - 1;
 
@@ -348,7 +361,7 @@ int64_t tile_attention_workspace(int32_t T, int32_t n_seqs, int32_t n_groups, in
   for (const TileList &l : s.list) {
     // Tiles are counted in 31 bits, a head's and a run's; the join's workgroups in 24.
     if (l.max_blocks > 0x7FFFFFFF / tiles / kv_heads) return -1;
-    if ((l.can_split || s.whole_rows > 0) && int64_t(l.max_blocks) * kv_heads * l.block_rows > kMostGroups) return -1;
+    if (s.whole_rows > 0 && int64_t(l.max_blocks) * kv_heads * join_chunks(l.block_rows) > kMostGroups) return -1;
   }
   TilePlan plan;
   return lay_out(s, n_groups + int64_t(n_seqs), head_dim, nullptr, &plan);
@@ -363,13 +376,14 @@ hipError_t launch_tile_attention(const TileAttention &a, hipStream_t stream) {
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && plan.list[0].max_blocks > 0) err = launch_tile_wide(a, plan, stream);
   if (err == hipSuccess && plan.list[1].max_blocks > 0) err = launch_tile_narrow(a, plan, stream);
+  const bool both = plan.whole_rows > 0;
   for (int i = 0; i < 2 && err == hipSuccess; ++i) {
     const TileList &l = plan.list[i];
-    if (l.max_blocks == 0 || !(l.can_split || plan.whole_rows > 0)) continue;
-    if (plan.whole_rows > 0 && i == 0) continue;      // the own places are in the narrow list
-    const int chunks = join_chunks(a, l.block_rows);
-    hipLaunchKernelGGL(tile_join_kernel, dim3(unsigned(int64_t(l.max_blocks) * hkv * chunks)), dim3(kJoinThreads), 0, stream,
-                       a, plan, i, chunks);
+    if (l.max_blocks == 0 || !(l.can_split || both) || (both && i == 0)) continue;
+    const int chunks = join_chunks(l.block_rows);
+    const int64_t blocks = both ? int64_t(l.max_blocks) * hkv : l.runs - 1;
+    hipLaunchKernelGGL(tile_join_kernel, dim3(unsigned(blocks * chunks)), dim3(kJoinThreads), 0, stream, a, plan, l, chunks,
+                       both);
     err = hipGetLastError();
   }
   return err;

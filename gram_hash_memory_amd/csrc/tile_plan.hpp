@@ -5,8 +5,8 @@
 // their prefix, or a sequence's one token over its own places.  Its query rows of
 // one key-value head (token-major, the heads of its group inside) are cut into
 // blocks, and the places that a block's rows see into tiles.  Problems of many rows
-// go to the wide list, whose blocks have 128 or 256 rows, one of 32 a wave: bound
-// by the matrix cores.  Problems of few go to the narrow list, whose blocks have 32
+// go to the wide list, whose blocks have 128 or 256 rows, 32 a wave: bound by the
+// matrix cores.  Problems of few go to the narrow list, whose blocks have 16 or 32
 // rows and whose waves share the places: bound by reading them.
 #pragma once
 
@@ -41,7 +41,7 @@ struct TileBlock {
   }
   // Whether any row sees place p.
   __device__ __forceinline__ bool used(int p) const {
-    return unsigned(p - b_lo) < unsigned(b_hi - b_lo) || unsigned(p - a_lo) < unsigned(a_hi - a_lo);
+    return (unsigned(p - b_lo) < unsigned(b_hi - b_lo)) | (unsigned(p - a_lo) < unsigned(a_hi - a_lo));
   }
 };
 
@@ -85,7 +85,7 @@ struct RowSees {
   int lo, n, first, m;
 };
 __device__ __forceinline__ bool sees(const RowSees &r, int p) {
-  return unsigned(p - r.lo) < unsigned(r.n) || unsigned(p - r.first) < unsigned(r.m);
+  return (unsigned(p - r.lo) < unsigned(r.n)) | (unsigned(p - r.first) < unsigned(r.m));
 }
 // The token at place `pos` of a sequence of `len` places.
 __device__ __forceinline__ RowSees row_sees(const AttentionRules &a, int seq, int token, int pos, int len) {
@@ -179,5 +179,7 @@ __device__ __forceinline__ bool next_block(const TileList &list, const TileHeade
 // tile_wide.hip, tile_narrow.hip: plan.list[0] and plan.list[1].
 hipError_t launch_tile_wide(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
 hipError_t launch_tile_narrow(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
+int tile_narrow_rows(int32_t head_dim, int64_t rows);              // of a block, for problems of so many
+int tile_narrow_groups(int32_t head_dim, int32_t block_rows);      // workgroups that run at once
 
 }  // namespace engram

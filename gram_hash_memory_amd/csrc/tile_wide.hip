@@ -323,7 +323,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             const int at = 8 * (x % 16 / 4) + x % 4, step = 32 * (x / 16) + at;
-            const bool ok = (unsigned(from_lo + step) < unsigned(r.n) || unsigned(from_first + step) < unsigned(r.m)) &&
+            const bool ok = ((unsigned(from_lo + step) < unsigned(r.n)) | (unsigned(from_first + step) < unsigned(r.m))) &
                             !(away[x / 16] & 1u << at);
             z[x / 16][x % 16] = ok ? z[x / 16][x % 16] : -INFINITY;
           }
