@@ -87,16 +87,17 @@ __device__ __forceinline__ float column_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// The values of dimensions d .. d + 3 of a place's row (d % 4 == 0).
+// The values of dimensions d .. d + 3 of a place's row (d % 4 == 0) of keys or values.
 template <bool kMx>
-__device__ __forceinline__ void values_at(const CacheView &c, int64_t row, int d, float *v) {
+__device__ __forceinline__ void values_at(const CacheView &c, const void *data, const uint8_t *scales, int64_t row, int d,
+                                          float *v) {
   if constexpr (kMx) {
-    const uint32_t codes = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(c.v) + row * c.head_dim + d);
-    const float scale = e8m0_to_float(min(uint32_t(c.v_scales[row * (c.head_dim / 32) + d / 32]), 254u));
+    const uint32_t codes = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(data) + row * c.head_dim + d);
+    const float scale = e8m0_to_float(min(uint32_t(scales[row * (c.head_dim / 32) + d / 32]), 254u));
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = e4m3fn_to_float(codes >> (8 * i) & 255u) * scale;
   } else {
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(c.v) + row * c.head_dim + d);
+    const u32x2 w = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(data) + row * c.head_dim + d);
     v[0] = bf16_lo(w[0]), v[1] = bf16_hi(w[0]), v[2] = bf16_lo(w[1]), v[3] = bf16_hi(w[1]);
   }
 }

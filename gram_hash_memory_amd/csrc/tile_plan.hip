@@ -18,7 +18,7 @@ using namespace attn;
 
 constexpr int kPlanThreads = 1024;
 constexpr int kWholePlaces = 512;          // contexts that are never cut
-constexpr int kJoinTiles[2] = {6, 3};      // what cutting costs, in tiles of a list
+constexpr int kWideJoin = 8, kNarrowJoin = 3;      // what cutting costs, in tiles of the list
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -116,10 +116,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
         w.first = w.len - n;
         const int t0 = w.row0 / group, t1 = (w.row0 + w.rows - 1) / group;
         int a_lo = 0x7FFFFFFF, a_hi = 0, b_lo = 0x7FFFFFFF, b_hi = 0;
+        w.all_hi = w.all_last = 0x7FFFFFFF;
         auto add = [&](int t) {
           const RowSees r = row_sees(a.rules, i, w.token0 + t, w.first + t, w.len);
           if (r.n > 0) b_lo = min(b_lo, r.lo), b_hi = max(b_hi, r.lo + r.n);
           if (r.m > 0) a_lo = min(a_lo, r.first), a_hi = max(a_hi, r.first + r.m);
+          w.all_lo = max(w.all_lo, r.lo), w.all_hi = min(w.all_hi, r.lo + r.n);
+          w.all_first = max(w.all_first, r.first), w.all_last = min(w.all_last, r.first + r.m);
         };
         if (a.rules.doc_starts) {
 #pragma unroll 8
@@ -133,11 +136,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
       } else if (i < a.n_groups) {
         w.kind = kSharedPrefix, w.seq = i;
         w.len = length_of(a.prefix_lens[i], a.max_prefix, a.prefix_width, a.cache.page_shift);
-        w.b_hi = w.len;
+        w.b_hi = w.all_hi = w.len;
       } else {
         w.kind = kOwnPlaces, w.seq = i - a.n_groups;
         w.len = length_of(a.lens[w.seq], a.max_len, a.table_width, a.cache.page_shift);
-        w.b_hi = w.len;
+        w.b_hi = w.all_hi = w.len;
         // The last group that does not begin behind the sequence.
         int lo = 0, hi = a.n_groups;
         while (lo < hi) {
@@ -159,8 +162,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
       w.b_tile = w.b_lo / list.tile;
       if (w.a_n > 0) w.b_tile = max(w.b_tile, w.a_tile + w.a_n);
       w.b_n = w.b_hi > 0 ? max(0, (w.b_hi - 1) / list.tile + 1 - w.b_tile) : 0;
-      // A chunk's rows that see nothing need their zeros: a tile without places.
-      if (w.kind == kChunk && w.tiles() == 0) w.b_n = 1;
+      // Rows that see nothing need their zeros: a tile without places.
+      if (w.kind != kOwnPlaces && w.tiles() == 0) w.b_n = 1;
       mine = w.tiles();
       longest = max(longest, mine);
     }
@@ -170,16 +173,30 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
     if (b < blocks) list.blocks[b] = w;
   }
   longest = max_all(longest);
+  // Whole blocks, those of most tiles first, take as long as their mean load and half
+  // a block, or as the longest one; runs as long as their share, and the join.
+  const int64_t pairs = int64_t(blocks) * a.cache.kv_heads;
+  const int64_t total = int64_t(units) * a.cache.kv_heads;
+  const int per = int(max(int64_t(1), (total + list.runs - 1) / list.runs));
+  const int64_t queued = max(int64_t(longest), pairs > list.runs ? per + units / blocks / 2 : int64_t(0));
+  const bool direct = !list.can_split || queued <= per + (blockIdx.x == 0 ? kWideJoin : kNarrowJoin);
   if (tid == 0) {
-    // Whole blocks off a queue take as long as their mean load and half a block, or
-    // as the longest one; runs as long as their share, and the join of its parts.
-    const int64_t pairs = int64_t(blocks) * a.cache.kv_heads;
-    const int64_t total = int64_t(units) * a.cache.kv_heads;
-    const int per = int(max(int64_t(1), (total + list.runs - 1) / list.runs));
-    const int64_t queued = max(int64_t(longest), pairs > list.runs ? per + longest / 2 : 0);
-    *list.header = TileHeader{units, blocks, per, !list.can_split || queued <= per + kJoinTiles[blockIdx.x]};
+    *list.header = TileHeader{units, blocks, per, direct};
     *list.queue = 0;
   }
+  if (!direct) return;
+  // The order: a count of each number of tiles, then each block's place.
+  __shared__ int bins[kPlanThreads];
+  bins[tid] = 0;
+  __syncthreads();
+  auto bin_of = [&](int b) { return kPlanThreads - 1 - min(kPlanThreads - 1, list.blocks[b].tiles()); };
+  for (int b = tid; b < blocks; b += kPlanThreads) atomicAdd(&bins[bin_of(b)], 1);
+  __syncthreads();
+  int all;
+  const int before = scan_before(bins[tid], &all);
+  bins[tid] = before;
+  __syncthreads();
+  for (int b = tid; b < blocks; b += kPlanThreads) list.order[atomicAdd(&bins[bin_of(b)], 1)] = b;
 }
 
 // ---------------------------------------------------------------- the join
@@ -292,19 +309,17 @@ Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int
   const int64_t problems = n_groups > 0 ? n_groups : n_seqs;
   TileList &wide = s.list[0], &narrow = s.list[1];
   // Few rows a problem on the average: all of them in narrow blocks.  Else narrow
-  // blocks for the problems that have no more than one, where there may be some
-  // whose places take long to read.
+  // blocks for the problems that have no more than one, where there may be several
+  // whose places take long to read (two more launches, some 5 us).
   const bool all_narrow = rows <= 2 * kRows * problems;
-  const bool some_narrow = all_narrow || n_groups > 0 || (n_seqs > 1 && max_len > 2 * kWholePlaces);
+  const bool some_narrow = all_narrow || n_groups > 0 || (n_seqs >= 8 && max_len > 2 * kWholePlaces);
   narrow.block_rows = tile_narrow_rows(head_dim, n_groups > 0 && !all_narrow ? group : ceil_div(rows, problems));
   narrow.tile = kNarrowTile;
   narrow.runs = tile_narrow_groups(head_dim, narrow.block_rows);
   s.narrow_rows = all_narrow ? 0x7FFFFFFF : some_narrow ? narrow.block_rows : 0;
-  // 8 waves where a problem has the rows for them and the registers suffice.
-  const int waves = head_dim <= 128 && rows > 4 * kRows * problems ? 8 : 4;
-  wide.block_rows = kRows * waves;
+  wide.block_rows = tile_wide_rows(head_dim, ceil_div(rows, problems));
   wide.tile = kWideTile;
-  wide.runs = waves == 8 || head_dim > 128 ? 256 : 512;
+  wide.runs = 256;                           // one a CU
   if (!all_narrow) wide.max_blocks = int32_t(std::min<int64_t>(0x7FFFFFFF, rows / wide.block_rows + problems));
   if (some_narrow) {
     const int64_t most = all_narrow ? rows / narrow.block_rows + problems : problems;
@@ -332,6 +347,8 @@ int64_t lay_out(const Sizes &s, int64_t problems, int64_t head_dim, uint8_t *bas
     l.queue = reinterpret_cast<int32_t *>(base + 128 * i + 64);
     l.blocks = reinterpret_cast<TileBlock *>(base + at);
     at += align256(l.max_blocks * int64_t(sizeof(TileBlock)));
+    l.order = reinterpret_cast<int32_t *>(base + at);
+    at += align256(int64_t(l.max_blocks) * 4);
     l.first_block = reinterpret_cast<int32_t *>(base + at);
     if (l.max_blocks > 0) at += align256(problems * 4);
     plan->list[i] = l;

@@ -32,6 +32,7 @@ struct TileBlock {
   int32_t a_lo, a_hi, b_lo, b_hi;
   int32_t a_tile, a_n, b_tile, b_n;
   int32_t before;                          // tiles of a head in the blocks before this one
+  int32_t all_lo, all_hi, all_first, all_last;     // all rows see [all_lo, all_hi) and [all_first, all_last)
   int32_t group, group_row;                // own places: the group (-1: none), the first row in it
 
   __device__ __forceinline__ int tiles() const { return a_n + b_n; }
@@ -49,7 +50,7 @@ struct TileHeader {
   int32_t units;                           // tiles of all blocks, of a head
   int32_t blocks;
   int32_t per;                             // tiles of a run
-  int32_t direct;                          // whole blocks off the queue instead of runs
+  int32_t direct;                          // whole blocks, those of most tiles first, instead of runs
 };
 
 // One list of blocks, in the workspace.
@@ -57,6 +58,7 @@ struct TileList {
   TileHeader *header;
   int32_t *queue;
   TileBlock *blocks;
+  int32_t *order;                          // the blocks by falling tiles (direct)
   int32_t *first_block;                    // of each problem of the list
   int32_t max_blocks, runs;                // workgroups
   int32_t block_rows, tile;
@@ -163,15 +165,17 @@ __device__ __forceinline__ bool first_work(const TileList &list, const TileHeade
 // The next whole block off the queue; false: none is left.
 __device__ __forceinline__ bool next_block(const TileList &list, const TileHeader &head, int kv_heads, int *lds,
                                            Work *w) {
-  if (threadIdx.x == 0) lds[0] = atomicAdd(list.queue, 1);
+  if (threadIdx.x == 0) {
+    const int at = atomicAdd(list.queue, 1);
+    lds[0] = at < head.blocks * kv_heads ? list.order[at / kv_heads] : -1;
+    lds[1] = at % kv_heads;
+  }
   __syncthreads();
-  const int at = __builtin_amdgcn_readfirstlane(lds[0]);
-  __syncthreads();
-  if (at >= head.blocks * kv_heads) return false;
-  w->block = head.blocks - 1 - at / kv_heads;        // a sequence's last blocks see most
-  w->kvh = at % kv_heads;
+  w->block = __builtin_amdgcn_readfirstlane(lds[0]);
+  w->kvh = __builtin_amdgcn_readfirstlane(lds[1]);
   w->unit = 0;
-  return true;
+  __syncthreads();
+  return w->block >= 0;
 }
 
 }  // namespace attn
@@ -179,7 +183,9 @@ __device__ __forceinline__ bool next_block(const TileList &list, const TileHeade
 // tile_wide.hip, tile_narrow.hip: plan.list[0] and plan.list[1].
 hipError_t launch_tile_wide(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
 hipError_t launch_tile_narrow(const TileAttention &a, const attn::TilePlan &plan, hipStream_t stream);
-int tile_narrow_rows(int32_t head_dim, int64_t rows);              // of a block, for problems of so many
+// Rows of a block, for problems of so many.
+int tile_wide_rows(int32_t head_dim, int64_t rows);
+int tile_narrow_rows(int32_t head_dim, int64_t rows);
 int tile_narrow_groups(int32_t head_dim, int32_t block_rows);      // workgroups that run at once
 
 }  // namespace engram

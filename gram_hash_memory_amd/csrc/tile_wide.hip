@@ -16,6 +16,8 @@
 //    the places in an order that V's transposing LDS reads follow.
 // Two workgroups' waves, or one's 8, share a SIMD: one's softmax fills the other's
 // waits for the matrix core.
+#include <cstddef>
+
 #include "attention_common.hpp"
 #include "tile_plan.hpp"
 
@@ -60,9 +62,16 @@ struct Stage {
   static constexpr int kBytes = kTile * (kKeyRow + kValueRow);
 };
 
+// What a workgroup works at next: a block, or a run's piece of one, of a key-value
+// head.  Wave 0 writes the tickets to LDS, a piece ahead.
+struct Ticket {
+  TileBlock w;
+  int32_t kvh, t0, count, flags;           // bit 0: there is one; bit 1: its whole block; bit 2: not the run's first
+};
+constexpr int kBlockWords = sizeof(TileBlock) / 4;
+
 template <int kDb, bool kMx, int kW, bool kRules>
-__global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
-    TileAttention a, TilePlan plan) {
+__global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(TileAttention a, TilePlan plan) {
   constexpr int D = 32 * kDb, kThreads = 64 * kW;
   constexpr int kRowBytes = kMx ? D : 2 * D;
   constexpr int kPieces = kRowBytes / 16, kLoads = (kTile * kPieces + kThreads - 1) / kThreads;
@@ -72,7 +81,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
   // Of the tiles in flight, by tile % 3: places on pages outside the cache, and
   // places whose values are not all finite.
   __shared__ uint32_t absent_lds[3][2], odd_lds[3][2];
-  __shared__ int4 limits_lds[kW];
+  __shared__ Ticket ticket_lds[4];
   __shared__ int work_lds[2];
 
   const CacheView &c = a.cache;
@@ -85,36 +94,196 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
   Work work;
   if (!first_work(list, head, c.kv_heads, kThreads, work_lds, &work)) return;
 
+  // Wave 0: ticket n's block is requested, and later written down.  Whole blocks are
+  // dealt out in their order, every second round backwards (but for the last three
+  // bits, which keep a head's blocks on one XCD).
+  int next_block = work.block, next_kvh = work.kvh, next_unit = work.unit, left = work.left, word = 0;
+  auto place_in_order = [&](int n) {
+    const int b = blockIdx.x;
+    return n * list.runs + (n % 2 && list.runs % 8 == 0 ? (list.runs - 8 - (b & ~7)) + (b & 7) : b);
+  };
+  auto ask_ticket = [&](int n) {
+    if (head.direct) {
+      const int e = place_in_order(n);
+      next_kvh = e % c.kv_heads;
+      next_block = e < head.blocks * c.kv_heads ? list.order[e / c.kv_heads] : -1;
+    } else if (left <= 0) {
+      next_block = -1;
+    }
+    if (next_block >= 0 && lane < kBlockWords) word = reinterpret_cast<const int *>(list.blocks + next_block)[lane];
+  };
+  auto write_ticket = [&](int n) {
+    Ticket &t = ticket_lds[n & 3];
+    const bool there = __builtin_amdgcn_readfirstlane(next_block) >= 0;
+    const int tiles = __builtin_amdgcn_readlane(word, offsetof(TileBlock, a_n) / 4) +
+                      __builtin_amdgcn_readlane(word, offsetof(TileBlock, b_n) / 4);
+    const int unit = head.direct ? 0 : next_unit, count = head.direct ? tiles : min(tiles - unit, left);
+    if (lane < kBlockWords) reinterpret_cast<int *>(&t.w)[lane] = word;
+    if (lane == 0) {
+      t.kvh = next_kvh, t.t0 = unit, t.count = count;
+      t.flags = (there ? 1 : 0) | (count == tiles ? 2 : 0) | (n > 0 ? 4 : 0);
+    }
+    if (!head.direct) {
+      left -= count;
+      next_unit = 0;
+      if (++next_block == head.blocks) next_block = 0, ++next_kvh;
+    }
+  };
+  if (wave == 0) {
+    ask_ticket(0);
+    write_ticket(0);
+    ask_ticket(1);
+    write_ticket(1);
+  }
+  if (tid < 6) absent_lds[tid / 2][tid % 2] = odd_lds[tid / 2][tid % 2] = 0;
+  __syncthreads();
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+
+  // Three tiles are under way: the pages of one are asked for, the keys and values of
+  // the one before it, and the one before that is worked at.  A piece's tiles follow
+  // those of the piece before it.
+  struct Tile {
+    int p0, kvh, flags;                      // flags: 1: there is one, 2: some row does not see all of it
+    uint64_t used;                           // bit i: some row sees place p0 + i
+  };
+  int ask_piece = -1, ask_t = 0, ask_t1 = 0;
+  TileBlock aw{};                            // what of the piece's block the tiles need
+  int ask_kvh = 0;
+  const int32_t *table = nullptr;
+  bool fetch = false;                        // a ticket has been asked for
+  auto range = [](int lo, int hi) {          // bits lo .. hi - 1, as far as there are any
+    lo = min(max(lo, 0), 64), hi = min(max(hi, lo), 64);
+    return (hi == 64 ? ~uint64_t(0) : (uint64_t(1) << hi) - 1) & (lo == 64 ? uint64_t(0) : ~uint64_t(0) << lo);
+  };
+  int page[kLoads];
+  auto ask_tile = [&]() {
+    if (ask_t == ask_t1) {
+      const Ticket &t = ticket_lds[(ask_piece + 1) & 3];
+      if (!(uniform(t.flags) & 1)) return Tile{0, 0, 0, 0};
+      ++ask_piece;
+      aw.kind = uniform(t.w.kind), aw.seq = uniform(t.w.seq), aw.len = uniform(t.w.len);
+      aw.a_lo = uniform(t.w.a_lo), aw.a_hi = uniform(t.w.a_hi), aw.b_lo = uniform(t.w.b_lo), aw.b_hi = uniform(t.w.b_hi);
+      aw.a_tile = uniform(t.w.a_tile), aw.a_n = uniform(t.w.a_n), aw.b_tile = uniform(t.w.b_tile);
+      aw.all_lo = uniform(t.w.all_lo), aw.all_hi = uniform(t.w.all_hi);
+      aw.all_first = uniform(t.w.all_first), aw.all_last = uniform(t.w.all_last);
+      ask_kvh = uniform(t.kvh), ask_t = uniform(t.t0), ask_t1 = ask_t + uniform(t.count);
+      table = aw.kind == kSharedPrefix ? a.prefix_table + int64_t(aw.seq) * a.prefix_width
+                                       : a.table + int64_t(aw.seq) * a.table_width;
+      if (aw.len == 0) table = list.queue;   // any memory: there is no place to look up
+      if (wave == 0 && ask_piece > 0) ask_ticket(ask_piece + 1);
+      fetch = ask_piece > 0;                 // the first two are written
+    }
+    const int p0 = aw.place(ask_t++, kTile), last = max(0, aw.len - 1);
+    const bool plain = (p0 >= aw.all_lo && p0 + kTile <= aw.all_hi) || (p0 >= aw.all_first && p0 + kTile <= aw.all_last);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) page[i] = table[min(p0 + (tid + i * kThreads) / kPieces, last) >> c.page_shift];
+    return Tile{p0, ask_kvh, plain ? 1 : 3, range(aw.a_lo - p0, aw.a_hi - p0) | range(aw.b_lo - p0, aw.b_hi - p0)};
+  };
+
+  // A thread's pieces of a tile: 16 bytes of keys and of values.
+  u32x4 key[kLoads], value[kLoads];
+  uint32_t scales[kLoads];                   // the key's and the value's byte (8-bit format)
+  uint32_t shown = 0;                        // bit i: piece i is of a place that is used, on a page
+  uint32_t missing = 0;                      // ... on no page of the cache
+  auto load = [&](const Tile &t) {
+    shown = missing = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kThreads, at = id % kPieces, in_tile = id / kPieces;
+      const bool in = (kTile * kPieces % kThreads == 0 || id < kTile * kPieces) && (t.used >> in_tile & 1);
+      const bool there = unsigned(page[i]) < unsigned(c.pages);
+      shown |= uint32_t(in & there) << i;
+      missing |= uint32_t(in & !there) << i;
+      // What is not there is read from the cache's first row instead, and not used.
+      const int64_t place = (in & there) ? ((int64_t(page[i]) * c.kv_heads + t.kvh) << c.page_shift) + ((t.p0 + in_tile) & mask) : 0;
+      key[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.k) + place * kRowBytes + 16 * at);
+      value[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.v) + place * kRowBytes + 16 * at);
+      if constexpr (kMx)
+        scales[i] = c.k_scales[place * kDb + at / 2] | uint32_t(c.v_scales[place * kDb + at / 2]) << 8;
+    }
+  };
+  auto put = [&](const Tile &tile, int t) {          // tile number t
+    uint8_t *const st = lds + t % 2 * S::kBytes;
+    const bool edge = tile.flags & 2;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kThreads, in_tile = id / kPieces, at = id % kPieces;
+      if (kTile * kPieces % kThreads != 0 && id >= kTile * kPieces) break;
+      constexpr int kOut = kMx ? 2 : 1;    // pieces of 8 values
+      u32x4 k[kOut], v[kOut];
+      if constexpr (kMx) {
+        const float ks = e8m0_to_float(scales[i] & 255u);
+        const float vs = e8m0_to_float(min(scales[i] >> 8, 254u));
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          k[x / 4][x % 4] = mx_pair(key[i][x / 2], ks, x & 1);
+          v[x / 4][x % 4] = mx_pair(value[i][x / 2], vs, x & 1);
+        }
+      } else {
+        k[0] = key[i], v[0] = value[i];
+      }
+      if (edge || missing) {
+        const bool keep = shown >> i & 1;
+        bool finite = true;
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            k[o][x] = keep ? k[o][x] : 0u;
+            v[o][x] = keep ? v[o][x] : 0u;
+            finite = finite & ((v[o][x] & 0x7F80u) != 0x7F80u) & ((v[o][x] & 0x7F800000u) != 0x7F800000u);
+          }
+        }
+        // A weight of 0 times a value that is not finite would reach rows that do
+        // not see it: it counts as 0 here, and add_odd() gives it to those that do.
+        if (!finite) {
+          atomicOr(&odd_lds[t % 3][in_tile / 32], 1u << (in_tile & 31));
+#pragma unroll
+          for (int o = 0; o < kOut; ++o)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if ((v[o][x] & 0x7F80u) == 0x7F80u) v[o][x] &= 0xFFFF0000u;
+              if ((v[o][x] & 0x7F800000u) == 0x7F800000u) v[o][x] &= 0xFFFFu;
+            }
+        }
+        if (missing >> i & 1) {
+          atomicOr(&absent_lds[t % 3][in_tile / 32], 1u << (in_tile & 31));
+          if (at == 0 && tile.kvh == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
+        }
+      }
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) {
+        *reinterpret_cast<u32x4 *>(st + in_tile * S::kKeyRow + (kOut * at + o) * 16) = k[o];
+        *reinterpret_cast<u32x4 *>(st + S::kValues + in_tile * S::kValueRow + (kOut * at + o) * 16) = v[o];
+      }
+    }
+  };
+
+  Tile now = ask_tile();
+  load(now);
+  Tile soon = ask_tile();                    // its pages; keys and values below
+  put(now, 0);
+  if (wave == 0 && fetch) write_ticket(ask_piece + 1);
+  fetch = false;
+  __syncthreads();
+
+  int t = 0;                                 // tiles since the start
   for (int piece = 0;; ++piece) {
-    if (head.direct && !next_block(list, head, c.kv_heads, work_lds, &work)) return;
-    const TileBlock w = list.blocks[work.block];
-    const int count = head.direct ? w.tiles() : min(w.tiles() - work.unit, work.left);
-    const bool whole = count == w.tiles();
-    const int kvh = work.kvh;
-    const bool shared = w.kind == kSharedPrefix;
-    const int32_t *table = shared ? a.prefix_table + int64_t(w.seq) * a.prefix_width
-                                  : a.table + int64_t(w.seq) * a.table_width;
+    const Ticket &ticket = ticket_lds[piece & 3];
+    const int flags = uniform(ticket.flags);
+    if (!(flags & 1)) return;
+    TileBlock w{};
+    w.kind = uniform(ticket.w.kind), w.seq = uniform(ticket.w.seq), w.token0 = uniform(ticket.w.token0);
+    w.first = uniform(ticket.w.first), w.row0 = uniform(ticket.w.row0), w.rows = uniform(ticket.w.rows);
+    w.len = uniform(ticket.w.len);
+    const int kvh = uniform(ticket.kvh), count = uniform(ticket.count);
+    const bool whole = flags & 2;
 
     // This lane's query row, and what it sees.
     const int row = wave * kRows + col;
-    const bool live = row < w.rows;
+    const bool active = wave * kRows < w.rows;
     const QueryRow qr = query_row(a, w, kvh, min(row, w.rows - 1));
     const int pos = w.first + qr.tok;
-    RowSees r{0, w.len, 0, 0};
-    if (w.kind == kChunk) r = row_sees(a.rules, w.seq, qr.token, pos, w.len);
-    const float slope = kRules && a.rules.slopes ? a.rules.slopes[qr.head] * kLog2e : 0.0f;
-    // A tile that all rows of a wave, or of the block, see needs no masks.
-    int4 lim = {r.lo, r.lo + r.n, r.first, r.first + r.m};
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-      lim.x = max(lim.x, __shfl_xor(lim.x, x));
-      lim.y = min(lim.y, __shfl_xor(lim.y, x));
-      lim.z = max(lim.z, __shfl_xor(lim.z, x));
-      lim.w = min(lim.w, __shfl_xor(lim.w, x));
-    }
-    if (lane == 0) limits_lds[wave] = lim;
-    if (tid < 6) absent_lds[tid / 2][tid % 2] = odd_lds[tid / 2][tid % 2] = 0;
-
     bf16x8 q[2 * kDb];
 #pragma unroll
     for (int kk = 0; kk < 2 * kDb; ++kk) {
@@ -123,132 +292,33 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
       for (int x = 0; x < 4; ++x) v[x] = (v[x] ^ su.flip) & su.keep;
       q[kk] = __builtin_bit_cast(bf16x8, v);
     }
-    const bool active = wave * kRows < w.rows;
-    __syncthreads();
-    int4 all = limits_lds[0];
+    RowSees r{0, w.len, 0, 0};
+    if (w.kind == kChunk) r = row_sees(a.rules, w.seq, qr.token, pos, w.len);
+    const float slope = kRules && a.rules.slopes ? a.rules.slopes[qr.head] * kLog2e : 0.0f;
+    // A tile that all rows of a wave see needs no masks.
+    int4 lim = {r.lo, r.lo + r.n, r.first, r.first + r.m};
 #pragma unroll
-    for (int x = 1; x < kW; ++x) {
-      const int4 y = limits_lds[x];
-      all = {max(all.x, y.x), min(all.y, y.y), max(all.z, y.z), min(all.w, y.w)};
+    for (int x = 1; x < 32; x *= 2) {
+      lim.x = max(lim.x, __shfl_xor(lim.x, x));
+      lim.y = min(lim.y, __shfl_xor(lim.y, x));
+      lim.z = max(lim.z, __shfl_xor(lim.z, x));
+      lim.w = min(lim.w, __shfl_xor(lim.w, x));
     }
-
-    auto place_of = [&](int t) { return w.place(t, kTile); };
-    auto plain = [&](const int4 &l, int p0) {
-      return (p0 >= l.x && p0 + kTile <= l.y) || (p0 >= l.z && p0 + kTile <= l.w);
-    };
-
-    // A thread's pieces of a tile: their pages, requested two tiles ahead, and
-    // their 16 bytes of keys and of values, one tile ahead.
-    int page[kLoads];
-    u32x4 key[kLoads], value[kLoads];
-    uint32_t scales[kLoads];                 // the key's and the value's byte (8-bit format)
-    uint32_t shown = 0;                      // bit i: piece i is of a place that is used, on a page
-    uint32_t missing = 0;                    // ... on no page of the cache
-    auto ask_pages = [&](int t) {
-      const int p0 = place_of(t);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int p = p0 + (tid + i * kThreads) / kPieces;
-        page[i] = w.len > 0 ? table[min(p, w.len - 1) >> c.page_shift] : -1;
-      }
-    };
-    auto load = [&](int t) {
-      const int p0 = place_of(t);
-      shown = missing = 0;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int id = tid + i * kThreads, p = p0 + id / kPieces, at = id % kPieces;
-        const bool in_tile = kTile * kPieces % kThreads == 0 || id < kTile * kPieces;
-        const bool in = in_tile && w.used(p), there = unsigned(page[i]) < unsigned(c.pages);
-        shown |= (in && there ? 1u : 0u) << i;
-        missing |= (in && !there ? 1u : 0u) << i;
-        // What is not there is read from the cache's first row instead, and not used.
-        const int64_t place = in && there
-            ? ((int64_t(page[i]) * c.kv_heads + kvh) << c.page_shift) + (p & mask) : 0;
-        key[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.k) + place * kRowBytes + 16 * at);
-        value[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.v) + place * kRowBytes + 16 * at);
-        if constexpr (kMx)
-          scales[i] = c.k_scales[place * kDb + at / 2] | uint32_t(c.v_scales[place * kDb + at / 2]) << 8;
-      }
-    };
-    auto put = [&](int t, int buf, bool edge) {
-      uint8_t *const st = lds + buf * S::kBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int id = tid + i * kThreads, in_tile = id / kPieces, at = id % kPieces;
-        if (kTile * kPieces % kThreads != 0 && id >= kTile * kPieces) break;
-        constexpr int kOut = kMx ? 2 : 1;    // pieces of 8 values
-        u32x4 k[kOut], v[kOut];
-        if constexpr (kMx) {
-          const float ks = e8m0_to_float(scales[i] & 255u);
-          const float vs = e8m0_to_float(min(scales[i] >> 8, 254u));
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            k[x / 4][x % 4] = mx_pair(key[i][x / 2], ks, x & 1);
-            v[x / 4][x % 4] = mx_pair(value[i][x / 2], vs, x & 1);
-          }
-        } else {
-          k[0] = key[i], v[0] = value[i];
-        }
-        if (edge || missing) {
-          const bool keep = shown >> i & 1;
-          bool finite = true;
-#pragma unroll
-          for (int o = 0; o < kOut; ++o) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              k[o][x] = keep ? k[o][x] : 0u;
-              v[o][x] = keep ? v[o][x] : 0u;
-              finite = finite && (v[o][x] & 0x7F80u) != 0x7F80u &&
-                       (v[o][x] & 0x7F800000u) != 0x7F800000u;
-            }
-          }
-          // A weight of 0 times a value that is not finite would reach rows that do
-          // not see it: it counts as 0 here, and add_odd() gives it to those that do.
-          if (!finite) {
-            atomicOr(&odd_lds[t % 3][in_tile / 32], 1u << (in_tile & 31));
-#pragma unroll
-            for (int o = 0; o < kOut; ++o)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                if ((v[o][x] & 0x7F80u) == 0x7F80u) v[o][x] &= 0xFFFF0000u;
-                if ((v[o][x] & 0x7F800000u) == 0x7F800000u) v[o][x] &= 0xFFFFu;
-              }
-          }
-          if (missing >> i & 1) {
-            atomicOr(&absent_lds[t % 3][in_tile / 32], 1u << (in_tile & 31));
-            if (at == 0 && kvh == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
-          }
-        }
-#pragma unroll
-        for (int o = 0; o < kOut; ++o) {
-          *reinterpret_cast<u32x4 *>(st + in_tile * S::kKeyRow + (kOut * at + o) * 16) = k[o];
-          *reinterpret_cast<u32x4 *>(st + S::kValues + in_tile * S::kValueRow + (kOut * at + o) * 16) = v[o];
-        }
-      }
-    };
+    lim = {uniform(lim.x), uniform(lim.y), uniform(lim.z), uniform(lim.w)};
+    auto plain = [&](int p0) { return (p0 >= lim.x && p0 + kTile <= lim.y) || (p0 >= lim.z && p0 + kTile <= lim.w); };
 
     float m = -INFINITY, l = 0.0f;           // l: of this lane's places
     f32x16 o[kDb];
 #pragma unroll
     for (int n = 0; n < kDb; ++n) o[n] = f32x16{};
 
-    const int t0 = work.unit, t1 = t0 + count;
-    ask_pages(t0);
-    load(t0);
-    ask_pages(min(t0 + 1, t1 - 1));
-    put(t0, 0, !plain(all, place_of(t0)));
-    __syncthreads();
-
-    for (int t = t0, buf = 0; t < t1; ++t, buf ^= 1) {
-      const int p0 = place_of(t);
-      if (t + 1 < t1) {
-        load(t + 1);
-        ask_pages(min(t + 2, t1 - 1));
-      }
+    for (int end = t + count; t < end; ++t) {
+      const int p0 = now.p0;
+      if (soon.flags) load(soon);
+      const Tile next = soon.flags ? ask_tile() : Tile{0, 0, 0, 0};
       // (tile + 2) % 3 was read before the last barrier, and is written after the next.
       if (tid < 2) absent_lds[(t + 2) % 3][tid] = odd_lds[(t + 2) % 3][tid] = 0;
-      const uint8_t *const st = lds + buf * S::kBytes;
+      const uint8_t *const st = lds + t % 2 * S::kBytes;
       const uint32_t absent[2] = {absent_lds[t % 3][0], absent_lds[t % 3][1]};
       const uint32_t odd[2] = {odd_lds[t % 3][0], odd_lds[t % 3][1]};
       const bool any_absent = __builtin_amdgcn_readfirstlane(absent[0] | absent[1]) != 0;
@@ -288,7 +358,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
           __builtin_amdgcn_sched_barrier(0);
         }
         // Register 4 i + j of tile half u: place 32 u + 8 i + 4 half + j.
-        const bool masked = !plain(lim, p0) || any_absent;
+        const bool masked = !plain(p0) || any_absent;
         if constexpr (kRules) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) z[x / 16][x % 16] *= su.unit;
@@ -378,7 +448,9 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
               if (x == i / 32 * 16 + (i & 31) / 8 * 4 + i % 4) e = z[x / 16][x % 16];
             e = __shfl(e, col + 32 * (i / 4 & 1));
             const int p = p0 + i;
-            const int pg = table[p >> c.page_shift];
+            const int32_t *const mine = w.kind == kSharedPrefix ? a.prefix_table + int64_t(w.seq) * a.prefix_width
+                                                                : a.table + int64_t(w.seq) * a.table_width;
+            const int pg = mine[p >> c.page_shift];
             const int64_t place = ((int64_t(pg) * c.kv_heads + kvh) << c.page_shift) + (p & mask);
             const bool ok = sees(r, p);
 #pragma unroll
@@ -386,7 +458,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 float v[4];
-                values_at<kMx>(c, place, 32 * n + 8 * x + 4 * half, v);
+                values_at<kMx>(c, c.v, c.v_scales, place, 32 * n + 8 * x + 4 * half, v);
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                   if (ok && !(fabsf(v[y]) < INFINITY)) o[n][4 * x + y] += e * v[y];
@@ -396,7 +468,11 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
           }
         }
       }
-      if (t + 1 < t1) put(t + 1, buf ^ 1, !plain(all, place_of(t + 1)));
+      if (soon.flags) put(soon, t + 1);
+      now = soon;
+      soon = next;
+      if (wave == 0 && fetch) write_ticket(ask_piece + 1);
+      fetch = false;
       __syncthreads();
     }
 
@@ -405,7 +481,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
       l = pair_sum(l);
       if (whole && plan.whole_rows == 0) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (live) {
+        if (row < w.rows) {
           if (a.lse && half == 0)
             a.lse[qr.at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
           uint16_t *const dst = a.out + qr.at * D + 4 * half;
@@ -417,10 +493,10 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
                   u32x2{pack_bf16x2(o[n][4 * i] * inv, o[n][4 * i + 1] * inv),
                         pack_bf16x2(o[n][4 * i + 2] * inv, o[n][4 * i + 3] * inv)};
         }
-      } else if (live) {
+      } else if (row < w.rows) {
         // A run's first piece, or a later one; or, whole, the row's own place.
-        const int64_t at = whole ? (shared ? int64_t(a.T) * a.q_heads : 0) + qr.at
-                                 : list.part_row(work.run, piece > 0, row);
+        const int64_t at = whole ? (w.kind == kSharedPrefix ? int64_t(a.T) * a.q_heads : 0) + qr.at
+                                 : list.part_row(work.run, flags & 4, row);
         if (half == 0) plan.ml[at] = float2{m, l};
         float *const dst = plan.o + at * D + 4 * half;
 #pragma unroll
@@ -430,12 +506,6 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(
             *reinterpret_cast<f32x4 *>(dst + 32 * n + 8 * i) =
                 f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
       }
-    }
-    if (!head.direct) {
-      work.left -= count;
-      if (work.left == 0) return;
-      work.unit = 0;
-      if (++work.block == head.blocks) work.block = 0, ++work.kvh;
     }
   }
 }
@@ -467,6 +537,8 @@ hipError_t by_format(const TileAttention &a, const TilePlan &plan, hipStream_t s
 }
 
 }  // namespace
+
+int tile_wide_rows(int32_t head_dim, int64_t rows) { return rows > 4 * kRows && head_dim <= 128 ? 8 * kRows : 4 * kRows; }
 
 hipError_t launch_tile_wide(const TileAttention &a, const TilePlan &plan, hipStream_t stream) {
   switch (a.cache.head_dim / 32) {
