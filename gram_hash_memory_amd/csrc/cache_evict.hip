@@ -16,7 +16,10 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 1024, kBins = 2048, kAtOnce = 4;
+constexpr int kThreads = 1024, kBins = 2048, kSlab = 4 * kThreads, kHeld = 8;
+
+// Four weights at any address of a weight.
+typedef float Unaligned4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // Whole numbers in the order of the weights: NaN lowest, -0 equal to 0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -66,9 +69,38 @@ __global__ __launch_bounds__(kThreads) void select_kernel(CacheEvict a) {
     return;
   }
 
-  // The first and the last places are above all weights.
+  // The first and the last places are above all weights.  A thread has 4 neighbouring
+  // places of every 4096; the first kHeld times 4096 stay in its registers.
   const int sinks = a.sinks, recent = len - a.recent;
-  auto key_at = [&](int p) { return p < sinks || p >= recent ? 0xFFFFFFFFu : key_of(weights[p]); };
+  auto keys_of = [&](const f32x4 &w, int p) {
+    u32x4 key;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key[j] = p + j < sinks || p + j >= recent ? 0xFFFFFFFFu : key_of(w[j]);
+    return key;
+  };
+  auto weights_at = [&](int p) {
+    f32x4 w{};
+    if (p + 4 <= len) {
+      w = *reinterpret_cast<const Unaligned4 *>(weights + p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (p + j < len) w[j] = weights[p + j];
+    }
+    return w;
+  };
+  const int slabs = (len + kSlab - 1) / kSlab;
+  f32x4 held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (i < slabs) held[i] = weights_at(i * kSlab + 4 * tid);
+  auto each_slab = [&](auto &&f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < slabs) f(i * kSlab + 4 * tid, held[i]);
+    for (int i = kHeld; i < slabs; ++i) f(i * kSlab + 4 * tid, weights_at(i * kSlab + 4 * tid));
+  };
+
   uint32_t want = uint32_t(count), limit = 0, known = 0;      // the want-th largest of those that begin as `limit`
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
@@ -76,19 +108,21 @@ __global__ __launch_bounds__(kThreads) void select_kernel(CacheEvict a) {
     const uint32_t digit = pass == 2 ? 0x3FFu : 0x7FFu;
     for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
     __syncthreads();
-    for (int base = 0; base < len; base += kThreads) {
-      const int p = base + tid;
-      const uint32_t key = p < len ? key_at(p) : 0;
-      const bool mine = p < len && (key & known) == limit;
-      const uint32_t bin = key >> shift & digit;
-      // Equal weights are common (none at all): one addition for a wave's most likely bin.
-      const uint64_t live = __ballot(mine);
-      if (live == 0) continue;
-      const uint32_t likely = __shfl(bin, __builtin_ctzll(live));
-      const uint64_t same = __ballot(mine && bin == likely);
-      if (mine && bin != likely) atomicAdd(&bins[bin], 1u);
-      if ((tid & 63) == 0) atomicAdd(&bins[likely], uint32_t(__popcll(same)));
-    }
+    each_slab([&](int p, const f32x4 &w) {
+      const u32x4 key = keys_of(w, p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool mine = p + j < len && (key[j] & known) == limit;
+        const uint32_t bin = key[j] >> shift & digit;
+        // Equal weights are common (none at all): one addition for a wave's most likely bin.
+        const uint64_t live = __ballot(mine);
+        if (live == 0) continue;
+        const uint32_t likely = __builtin_amdgcn_readlane(bin, __builtin_ctzll(live));
+        const uint64_t same = __ballot(mine && bin == likely);
+        if (mine && bin != likely) atomicAdd(&bins[bin], 1u);
+        if ((tid & 63) == 0) atomicAdd(&bins[likely], uint32_t(__popcll(same)));
+      }
+    });
     __syncthreads();
     // Bins from the highest on: thread i has 2047 - 2 i and 2046 - 2 i.
     const uint32_t hi = bins[kBins - 1 - 2 * tid], lo = bins[kBins - 2 - 2 * tid];
@@ -106,30 +140,28 @@ __global__ __launch_bounds__(kThreads) void select_kernel(CacheEvict a) {
 
   // Those above the limit, and the first `want` of those equal to it.
   uint32_t above = 0, equal = 0;
-  for (int base = 0; base < len; base += kThreads * kAtOnce) {
-    const int p0 = base + kAtOnce * tid;
-    uint32_t key[kAtOnce], mine = 0;         // equal ones in the upper half, above it in the lower
+  each_slab([&](int p, const f32x4 &w) {
+    const u32x4 key = keys_of(w, p);
+    uint32_t mine = 0;                       // equal ones in the upper half, above it in the lower
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      key[j] = p0 + j < len ? key_at(p0 + j) : 0;
-      if (p0 + j < len) mine += key[j] > limit ? 1u : key[j] == limit ? 0x10000u : 0u;
-    }
+    for (int j = 0; j < 4; ++j)
+      if (p + j < len) mine += key[j] > limit ? 1u : key[j] == limit ? 0x10000u : 0u;
     uint32_t total;
     const uint32_t before = scan_before(mine, scan_lds, &total);
     uint32_t up = above + (before & 0xFFFFu), eq = equal + (before >> 16);
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      if (p0 + j >= len) break;
+    for (int j = 0; j < 4; ++j) {
+      if (p + j >= len) break;
       const bool is_above = key[j] > limit, is_equal = key[j] == limit;
       if (is_above || (is_equal && eq < want)) {
         const uint32_t at = up + min(eq, want);
-        kept[at] = p0 + j;
-        new_weights[at] = weights[p0 + j];
+        kept[at] = p + j;
+        new_weights[at] = w[j];
       }
       up += is_above, eq += is_equal;
     }
     above += total & 0xFFFFu, equal += total >> 16;
-  }
+  });
 }
 
 constexpr int kMoveThreads = 256;

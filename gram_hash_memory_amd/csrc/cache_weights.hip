@@ -18,7 +18,7 @@ using namespace attn;
 constexpr int kWaves = 4, kPlaces = 32;      // of a wave
 
 template <int kDb, bool kMx>
-__global__ __launch_bounds__(64 * kWaves) void cache_weights_kernel(CacheWeights a, int chunks) {
+__global__ __launch_bounds__(64 * kWaves, kDb <= 4 ? 4 : 2) void cache_weights_kernel(CacheWeights a, int chunks) {
   constexpr int D = 32 * kDb, kRowBytes = kMx ? D : 2 * D;
   const CacheView &c = a.cache;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -40,23 +40,60 @@ __global__ __launch_bounds__(64 * kWaves) void cache_weights_kernel(CacheWeights
   }
   if (t0 >= t1) return;
 
+  // 16 query rows as B operands, with what they see: requested before the keys, and
+  // the next 16 before these are used.
+  struct Rows {
+    bf16x8 q[kDb];
+    RowSees sees;
+    float lse, slope;
+    int pos;
+    bool live;
+  };
+  const int r1 = t1 * group;
+  auto load_rows = [&](int r0, Rows &x) {
+    const int row = min(r0 + col, r1 - 1), tok = row / group, token = begin + tok;
+    const int head = kvh * group + row - tok * group;
+    const int64_t q_row = int64_t(token) * a.q_heads + head;
+#pragma unroll
+    for (int kk = 0; kk < kDb; ++kk) {
+      const int d = kMx && (kk | 1) < kDb ? 64 * (kk / 2) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
+      x.q[kk] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(a.q + q_row * D + d));
+    }
+    x.pos = first + tok;
+    x.sees = row_sees(a.rules, s, token, x.pos, len);
+    x.lse = a.lse[q_row];
+    x.slope = a.rules.slopes ? a.rules.slopes[head] * kLog2e : 0.0f;
+    x.live = r0 + col < r1;
+  };
+  Rows rows[2];
+  load_rows(t0 * group, rows[0]);
+  // What is to be added to: lanes col < 8 write a place each.
+  const int out_p = p0 + 16 * (col / 4) + 4 * g + col % 4;
+  float *const out = a.weights + pair * a.weights_stride + out_p;
+  const bool writes = col < 8 && out_p < len;
+  const float old = writes ? *out : 0.0f;
+
   // Keys: place 16 u + col, as A operands.  In the 8-bit format 16 bytes are two steps.
   bf16x8 k[2][kDb];
   uint32_t absent = 0;                       // bit 16 u + x: place 16 u + x is on no page of the cache
+  int64_t place[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int p = p0 + 16 * u + col;
     const int page = p < len ? a.table[int64_t(s) * a.table_width + (p >> c.page_shift)] : -1;
     const bool there = unsigned(page) < unsigned(c.pages);
     absent |= uint32_t(__ballot(!there) & 0xFFFFu) << (16 * u);
-    const int64_t place = there ? ((int64_t(page) * c.kv_heads + kvh) << c.page_shift) + (p & mask) : 0;
-    const uint8_t *const src = static_cast<const uint8_t *>(c.k) + place * kRowBytes;
+    place[u] = there ? ((int64_t(page) * c.kv_heads + kvh) << c.page_shift) + (p & mask) : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t *const src = static_cast<const uint8_t *>(c.k) + place[u] * kRowBytes;
     if constexpr (!kMx) {
 #pragma unroll
       for (int kk = 0; kk < kDb; ++kk)
         k[u][kk] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(src + 64 * kk + 16 * g));
     } else {
-      const uint8_t *const sc = c.k_scales + place * kDb;
+      const uint8_t *const sc = c.k_scales + place[u] * kDb;
       u32x4 code[(kDb + 1) / 2];
       float scale[(kDb + 1) / 2];
 #pragma unroll
@@ -82,38 +119,36 @@ __global__ __launch_bounds__(64 * kWaves) void cache_weights_kernel(CacheWeights
   const float cap2 = a.rules.cap * kLog2e;
   f32x4 sum[2] = {};
   bool bad = false;
-  const int r1 = t1 * group;
-  for (int r0 = t0 * group; r0 < r1; r0 += 16) {
-    const int row = min(r0 + col, r1 - 1), tok = row / group, token = begin + tok;
-    const int head = kvh * group + row - tok * group;
-    const int64_t q_row = int64_t(token) * a.q_heads + head;
-    const uint16_t *const src = a.q + q_row * D;
+  auto add_rows = [&](const Rows &x) {
     f32x4 z[2] = {};
 #pragma unroll
-    for (int kk = 0; kk < kDb; ++kk) {
-      const int d = kMx && (kk | 1) < kDb ? 64 * (kk / 2) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
-      const bf16x8 q = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(src + d));
+    for (int kk = 0; kk < kDb; ++kk)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) z[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][kk], q, z[u], 0, 0, 0);
-    }
-    const int pos = first + tok;
-    const RowSees r = row_sees(a.rules, s, token, pos, len);
-    const float lse = a.lse[q_row] * kLog2e;
-    const bool live = r0 + col < r1 && lse != -INFINITY;
-    const float slope = a.rules.slopes ? a.rules.slopes[head] * kLog2e : 0.0f;
+      for (int u = 0; u < 2; ++u) z[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][kk], x.q[kk], z[u], 0, 0, 0);
+    const bool weighs = x.lse != -INFINITY;
+    const float lse = weighs ? x.lse * kLog2e : 0.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int at = 16 * u + 4 * g + j, p = p0 + at;
-        float x = z[u][j] * unit;
-        if (a.rules.cap > 0.0f) x = cap2 * (fabsf(x) <= kTanhSplit ? tanh_small(x) : tanh_large(x));
-        if (a.rules.slopes) x = __builtin_fmaf(-slope, float(abs(pos - p)), x);
-        const bool seen = r0 + col < r1 && sees(r, p);
-        bad |= seen && (absent >> at & 1);
-        const float e = __builtin_amdgcn_exp2f(x - lse);
-        sum[u][j] += seen && live && !(absent >> at & 1) ? e : 0.0f;
+        float y = z[u][j] * unit;
+        if (a.rules.cap > 0.0f) {
+          const float small = tanh_small(y), large = tanh_large(y);
+          y = cap2 * (fabsf(y) <= kTanhSplit ? small : large);
+        }
+        if (a.rules.slopes) y = __builtin_fmaf(-x.slope, float(abs(x.pos - p)), y);
+        const bool seen = x.live & sees(x.sees, p), gone = absent >> at & 1;
+        bad |= seen & gone;
+        const float e = __builtin_amdgcn_exp2f(y - lse);
+        sum[u][j] += (seen & weighs & !gone) ? e : 0.0f;
       }
+  };
+  for (int r0 = t0 * group; r0 < r1; r0 += 32) {
+    if (r0 + 16 < r1) load_rows(r0 + 16, rows[1]);
+    add_rows(rows[0]);
+    if (r0 + 32 < r1) load_rows(r0 + 32, rows[0]);
+    if (r0 + 16 < r1) add_rows(rows[1]);
   }
   if (bad && kvh == 0 && a.bad_pages) atomicAdd(a.bad_pages, 1);
 
@@ -128,11 +163,7 @@ __global__ __launch_bounds__(64 * kWaves) void cache_weights_kernel(CacheWeights
       for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d);
       if (col == 4 * u + j) mine = x;
     }
-  const int p = p0 + 16 * (col / 4) + 4 * g + col % 4;
-  if (col < 8 && p < len) {
-    float *const w = a.weights + pair * a.weights_stride + p;
-    *w += mine;
-  }
+  if (writes) *out = old + mine;
 }
 
 template <int kDb>

@@ -99,9 +99,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
   blocks = min(blocks, list.max_blocks);     // more only where cu does not rise
   __syncthreads();
 
+  // With documents 8 neighbouring threads look at a block's tokens.
+  const int threads = a.rules.doc_starts ? 8 : 1, sub = tid % threads;
   int units = 0, longest = 0;
-  for (int base = 0; base < blocks; base += kPlanThreads) {
-    const int b = base + tid;
+  for (int base = 0; base < blocks; base += kPlanThreads / threads) {
+    const int b = base + tid / threads;
     int mine = 0;
     TileBlock w{};
     if (b < blocks) {
@@ -124,9 +126,17 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
           w.all_lo = max(w.all_lo, r.lo), w.all_hi = min(w.all_hi, r.lo + r.n);
           w.all_first = max(w.all_first, r.first), w.all_last = min(w.all_last, r.first + r.m);
         };
-        if (a.rules.doc_starts) {
+        if (threads > 1) {
 #pragma unroll 8
-          for (int t = t0; t <= t1; ++t) add(t);
+          for (int t = t0 + sub; t <= t1; t += 8) add(t);
+#pragma unroll
+          for (int x = 1; x < 8; x *= 2) {
+            a_lo = min(a_lo, __shfl_xor(a_lo, x)), a_hi = max(a_hi, __shfl_xor(a_hi, x));
+            b_lo = min(b_lo, __shfl_xor(b_lo, x)), b_hi = max(b_hi, __shfl_xor(b_hi, x));
+            w.all_lo = max(w.all_lo, __shfl_xor(w.all_lo, x)), w.all_hi = min(w.all_hi, __shfl_xor(w.all_hi, x));
+            w.all_first = max(w.all_first, __shfl_xor(w.all_first, x));
+            w.all_last = min(w.all_last, __shfl_xor(w.all_last, x));
+          }
         } else {                             // the first token sees the first place, the last one the last
           add(t0);
           add(t1);
@@ -164,13 +174,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
       w.b_n = w.b_hi > 0 ? max(0, (w.b_hi - 1) / list.tile + 1 - w.b_tile) : 0;
       // Rows that see nothing need their zeros: a tile without places.
       if (w.kind != kOwnPlaces && w.tiles() == 0) w.b_n = 1;
-      mine = w.tiles();
+      mine = sub == 0 ? w.tiles() : 0;
       longest = max(longest, mine);
     }
     int total;
     w.before = units + scan_before(mine, &total);
     units += total;
-    if (b < blocks) list.blocks[b] = w;
+    if (b < blocks && sub == 0) list.blocks[b] = w;
   }
   longest = max_all(longest);
   // Whole blocks, those of most tiles first, take as long as their mean load and half

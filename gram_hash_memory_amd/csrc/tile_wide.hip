@@ -33,6 +33,35 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Accumulators that the wave's own instructions scale or add to, rarely.  In large
+// heads they are to stay where the matrix core has them: left to itself the compiler
+// moves all of them to and fro around each of its products.  A product's result takes
+// up to 18 waits to be readable by other instructions, and what is written there some
+// before it is read.
+template <bool kKeep>
+__device__ __forceinline__ void scale(f32x16 &o, float by) {
+  if constexpr (!kKeep) {
+    o *= by;
+  } else {
+    asm volatile("s_nop 15\n\ts_nop 7");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x = o[i], y;
+      asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1\n\ts_nop 3"
+                   : "+a"(x), "=&v"(y) : "v"(by));
+      o[i] = x;
+    }
+  }
+}
+template <bool kKeep>
+__device__ __forceinline__ float plus(float o, float more) {
+  if constexpr (!kKeep) return o + more;
+  float y;
+  asm volatile("s_nop 15\n\ts_nop 7\n\tv_accvgpr_read_b32 %1, %0\n\tv_add_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1\n\ts_nop 3"
+               : "+a"(o), "=&v"(y) : "v"(more));
+  return o;
+}
+
 // Over lanes l and l ^ 32, which hold one query row.
 __device__ __forceinline__ float pair_max(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -74,7 +103,10 @@ template <int kDb, bool kMx, int kW, bool kRules>
 __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(TileAttention a, TilePlan plan) {
   constexpr int D = 32 * kDb, kThreads = 64 * kW;
   constexpr int kRowBytes = kMx ? D : 2 * D;
-  constexpr int kPieces = kRowBytes / 16, kLoads = (kTile * kPieces + kThreads - 1) / kThreads;
+  // Large heads' tiles are staged in two rounds, for want of registers.
+  constexpr int kPieces = kRowBytes / 16, kRounds = !kMx && kTile * kPieces > 3 * kThreads ? 2 : 1, kPart = kTile / kRounds;
+  constexpr int kLoads = (kPart * kPieces + kThreads - 1) / kThreads;
+  constexpr bool kKeep = kDb > 4;
   using S = Stage<kDb>;
   extern __shared__ u32x4 stages_lds[];      // [2] stages
   uint8_t *const lds = reinterpret_cast<uint8_t *>(stages_lds);
@@ -155,7 +187,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
     lo = min(max(lo, 0), 64), hi = min(max(hi, lo), 64);
     return (hi == 64 ? ~uint64_t(0) : (uint64_t(1) << hi) - 1) & (lo == 64 ? uint64_t(0) : ~uint64_t(0) << lo);
   };
-  int page[kLoads];
+  int page[kRounds][kLoads];
   auto ask_tile = [&]() {
     if (ask_t == ask_t1) {
       const Ticket &t = ticket_lds[(ask_piece + 1) & 3];
@@ -176,7 +208,10 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
     const int p0 = aw.place(ask_t++, kTile), last = max(0, aw.len - 1);
     const bool plain = (p0 >= aw.all_lo && p0 + kTile <= aw.all_hi) || (p0 >= aw.all_first && p0 + kTile <= aw.all_last);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) page[i] = table[min(p0 + (tid + i * kThreads) / kPieces, last) >> c.page_shift];
+    for (int x = 0; x < kRounds; ++x)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        page[x][i] = table[min(p0 + kPart * x + (tid + i * kThreads) / kPieces, last) >> c.page_shift];
     return Tile{p0, ask_kvh, plain ? 1 : 3, range(aw.a_lo - p0, aw.a_hi - p0) | range(aw.b_lo - p0, aw.b_hi - p0)};
   };
 
@@ -185,30 +220,30 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
   uint32_t scales[kLoads];                   // the key's and the value's byte (8-bit format)
   uint32_t shown = 0;                        // bit i: piece i is of a place that is used, on a page
   uint32_t missing = 0;                      // ... on no page of the cache
-  auto load = [&](const Tile &t) {
+  auto load = [&](const Tile &t, int round) {
     shown = missing = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int id = tid + i * kThreads, at = id % kPieces, in_tile = id / kPieces;
-      const bool in = (kTile * kPieces % kThreads == 0 || id < kTile * kPieces) && (t.used >> in_tile & 1);
-      const bool there = unsigned(page[i]) < unsigned(c.pages);
+      const int id = tid + i * kThreads, at = id % kPieces, in_tile = kPart * round + id / kPieces;
+      const bool in = (kPart * kPieces % kThreads == 0 || id < kPart * kPieces) && (t.used >> in_tile & 1);
+      const bool there = unsigned(page[round][i]) < unsigned(c.pages);
       shown |= uint32_t(in & there) << i;
       missing |= uint32_t(in & !there) << i;
       // What is not there is read from the cache's first row instead, and not used.
-      const int64_t place = (in & there) ? ((int64_t(page[i]) * c.kv_heads + t.kvh) << c.page_shift) + ((t.p0 + in_tile) & mask) : 0;
+      const int64_t place = (in & there) ? ((int64_t(page[round][i]) * c.kv_heads + t.kvh) << c.page_shift) + ((t.p0 + in_tile) & mask) : 0;
       key[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.k) + place * kRowBytes + 16 * at);
       value[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(c.v) + place * kRowBytes + 16 * at);
       if constexpr (kMx)
         scales[i] = c.k_scales[place * kDb + at / 2] | uint32_t(c.v_scales[place * kDb + at / 2]) << 8;
     }
   };
-  auto put = [&](const Tile &tile, int t) {          // tile number t
+  auto put = [&](const Tile &tile, int t, int round) {       // tile number t
     uint8_t *const st = lds + t % 2 * S::kBytes;
     const bool edge = tile.flags & 2;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int id = tid + i * kThreads, in_tile = id / kPieces, at = id % kPieces;
-      if (kTile * kPieces % kThreads != 0 && id >= kTile * kPieces) break;
+      const int id = tid + i * kThreads, in_tile = kPart * round + id / kPieces, at = id % kPieces;
+      if (kPart * kPieces % kThreads != 0 && id >= kPart * kPieces) break;
       constexpr int kOut = kMx ? 2 : 1;    // pieces of 8 values
       u32x4 k[kOut], v[kOut];
       if constexpr (kMx) {
@@ -260,9 +295,12 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
   };
 
   Tile now = ask_tile();
-  load(now);
+#pragma unroll
+  for (int x = 0; x < kRounds; ++x) {
+    load(now, x);
+    put(now, 0, x);
+  }
   Tile soon = ask_tile();                    // its pages; keys and values below
-  put(now, 0);
   if (wave == 0 && fetch) write_ticket(ask_piece + 1);
   fetch = false;
   __syncthreads();
@@ -314,8 +352,9 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
 
     for (int end = t + count; t < end; ++t) {
       const int p0 = now.p0;
-      if (soon.flags) load(soon);
-      const Tile next = soon.flags ? ask_tile() : Tile{0, 0, 0, 0};
+      const Tile coming = soon;
+      if (coming.flags) load(coming, 0);
+      if (kRounds == 1 && coming.flags) soon = ask_tile();
       // (tile + 2) % 3 was read before the last barrier, and is written after the next.
       if (tid < 2) absent_lds[(t + 2) % 3][tid] = odd_lds[(t + 2) % 3][tid] = 0;
       const uint8_t *const st = lds + t % 2 * S::kBytes;
@@ -324,6 +363,14 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
       const bool any_absent = __builtin_amdgcn_readfirstlane(absent[0] | absent[1]) != 0;
       const bool any_odd = __builtin_amdgcn_readfirstlane(odd[0] | odd[1]) != 0;
 
+      auto stage_rest = [&] {                // the second round, as a part of the work on the tile before
+        if (kRounds == 2 && coming.flags) {
+          put(coming, t + 1, 0);
+          load(coming, 1);
+          soon = ask_tile();
+        }
+      };
+      if (!active) stage_rest();
       if (active) {
         // Operands come 4 at a time, each four requested before the four before it
         // are used: more would not fit the registers.
@@ -357,6 +404,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
           for (int x = 0; x < 4; ++x) z[x % 2] = mfma32(kf[i % 2][x], q[2 * i + x / 2], z[x % 2]);
           __builtin_amdgcn_sched_barrier(0);
         }
+        stage_rest();
         // Register 4 i + j of tile half u: place 32 u + 8 i + 4 half + j.
         const bool masked = !plain(p0) || any_absent;
         if constexpr (kRules) {
@@ -409,7 +457,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
           m = mn;
           l *= keep;
 #pragma unroll
-          for (int n = 0; n < kDb; ++n) o[n] *= keep;
+          for (int n = 0; n < kDb; ++n) scale<kKeep>(o[n], keep);
         }
         const float ms = m == -INFINITY ? 0.0f : m;
         float sum[2] = {};
@@ -461,16 +509,16 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
                 values_at<kMx>(c, c.v, c.v_scales, place, 32 * n + 8 * x + 4 * half, v);
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                  if (ok && !(fabsf(v[y]) < INFINITY)) o[n][4 * x + y] += e * v[y];
+                  o[n][4 * x + y] = plus<kKeep>(o[n][4 * x + y], ok && !(fabsf(v[y]) < INFINITY) ? e * v[y] : 0.0f);
               }
               __builtin_amdgcn_sched_barrier(0);      // no more of these loads at a time: registers
             }
           }
         }
       }
-      if (soon.flags) put(soon, t + 1);
-      now = soon;
-      soon = next;
+      if (coming.flags) put(coming, t + 1, kRounds - 1);
+      else soon = Tile{0, 0, 0, 0};
+      now = coming;
       if (wave == 0 && fetch) write_ticket(ask_piece + 1);
       fetch = false;
       __syncthreads();
