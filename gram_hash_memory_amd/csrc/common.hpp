@@ -245,7 +245,7 @@ struct CacheWeights {
   int32_t T, n_seqs, q_heads, table_width, max_len;
   float scale;
 };
-int64_t cache_weights_blocks(int32_t n_seqs, int32_t kv_heads, int32_t max_len);
+int64_t cache_weights_blocks(int32_t n_seqs, int32_t kv_heads, int32_t max_len);      // at most
 hipError_t launch_cache_weights(const CacheWeights &a, hipStream_t stream);
 
 struct CacheEvict {

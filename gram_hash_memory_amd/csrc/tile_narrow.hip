@@ -51,7 +51,7 @@ __device__ __forceinline__ void work_piece(const TileAttention &a, const TilePla
     const QueryRow qr = query_row(a, w, kvh, min(16 * t + col, w.rows - 1));
     pos[t] = w.first + qr.tok;
     r[t] = RowSees{0, w.len, 0, 0};
-    if (w.kind == kChunk) r[t] = row_sees(a.rules, w.seq, qr.token, pos[t], w.len);
+    if (w.kind == kChunk) r[t] = token_sees(a.rules, w.seq, qr.token, pos[t], w.len);
     slope[t] = a.rules.slopes ? a.rules.slopes[qr.head] * kLog2e : 0.0f;
     lim = {max(lim.x, r[t].lo), min(lim.y, r[t].lo + r[t].n), max(lim.z, r[t].first), min(lim.w, r[t].first + r[t].m)};
 #pragma unroll

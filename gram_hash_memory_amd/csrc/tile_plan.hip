@@ -119,16 +119,22 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
         const int t0 = w.row0 / group, t1 = (w.row0 + w.rows - 1) / group;
         int a_lo = 0x7FFFFFFF, a_hi = 0, b_lo = 0x7FFFFFFF, b_hi = 0;
         w.all_hi = w.all_last = 0x7FFFFFFF;
-        auto add = [&](int t) {
-          const RowSees r = row_sees(a.rules, i, w.token0 + t, w.first + t, w.len);
+        const int prefix = prefix_of(a.rules, i, w.len);
+        auto add = [&](int t, int doc) {
+          const RowSees r = row_sees(a.rules, prefix, doc, w.first + t, w.len);
           if (r.n > 0) b_lo = min(b_lo, r.lo), b_hi = max(b_hi, r.lo + r.n);
           if (r.m > 0) a_lo = min(a_lo, r.first), a_hi = max(a_hi, r.first + r.m);
           w.all_lo = max(w.all_lo, r.lo), w.all_hi = min(w.all_hi, r.lo + r.n);
           w.all_first = max(w.all_first, r.first), w.all_last = min(w.all_last, r.first + r.m);
         };
         if (threads > 1) {
-#pragma unroll 8
-          for (int t = t0 + sub; t <= t1; t += 8) add(t);
+          for (int t = t0 + sub; t <= t1; t += 64) {
+            int doc[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) doc[x] = a.rules.doc_starts[w.token0 + min(t + 8 * x, t1)];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) add(min(t + 8 * x, t1), doc[x]);
+          }
 #pragma unroll
           for (int x = 1; x < 8; x *= 2) {
             a_lo = min(a_lo, __shfl_xor(a_lo, x)), a_hi = max(a_hi, __shfl_xor(a_hi, x));
@@ -138,8 +144,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
             w.all_last = min(w.all_last, __shfl_xor(w.all_last, x));
           }
         } else {                             // the first token sees the first place, the last one the last
-          add(t0);
-          add(t1);
+          add(t0, 0);
+          add(t1, 0);
         }
         if (a_hi > 0) w.a_lo = a_lo, w.a_hi = a_hi;
         if (b_hi > 0) w.b_lo = b_lo, w.b_hi = b_hi;

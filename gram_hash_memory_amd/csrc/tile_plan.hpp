@@ -89,15 +89,22 @@ struct RowSees {
 __device__ __forceinline__ bool sees(const RowSees &r, int p) {
   return (unsigned(p - r.lo) < unsigned(r.n)) | (unsigned(p - r.first) < unsigned(r.m));
 }
-// The token at place `pos` of a sequence of `len` places.
-__device__ __forceinline__ RowSees row_sees(const AttentionRules &a, int seq, int token, int pos, int len) {
-  const int doc = a.doc_starts ? max(0, a.doc_starts[token]) : 0;
+// The places of its prefix that sequence `seq` of `len` places has.
+__device__ __forceinline__ int prefix_of(const AttentionRules &a, int seq, int len) {
+  return a.prefix_lens ? max(0, min(a.prefix_lens[seq], len)) : 0;
+}
+// The token at place `pos` of a sequence of `len` places, whose document begins at `doc`.
+__device__ __forceinline__ RowSees row_sees(const AttentionRules &a, int prefix, int doc, int pos, int len) {
+  doc = max(0, doc);
   RowSees r;
   r.lo = max(doc, a.window > 0 ? pos - a.window + 1 : 0);
   r.n = max(0, max(0, min(pos + 1, len)) - r.lo);
   r.first = doc;
-  r.m = max(0, (a.prefix_lens ? max(0, min(a.prefix_lens[seq], len)) : 0) - doc);
+  r.m = max(0, prefix - doc);
   return r;
+}
+__device__ __forceinline__ RowSees token_sees(const AttentionRules &a, int seq, int token, int pos, int len) {
+  return row_sees(a, prefix_of(a, seq, len), a.doc_starts ? a.doc_starts[token] : 0, pos, len);
 }
 
 // A sequence's length as the kernels take it.

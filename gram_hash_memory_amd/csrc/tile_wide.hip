@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * kW, kDb <= 4 ? 2 : 1) void tile_wide_kernel(Ti
       q[kk] = __builtin_bit_cast(bf16x8, v);
     }
     RowSees r{0, w.len, 0, 0};
-    if (w.kind == kChunk) r = row_sees(a.rules, w.seq, qr.token, pos, w.len);
+    if (w.kind == kChunk) r = token_sees(a.rules, w.seq, qr.token, pos, w.len);
     const float slope = kRules && a.rules.slopes ? a.rules.slopes[qr.head] * kLog2e : 0.0f;
     // A tile that all rows of a wave see needs no masks.
     int4 lim = {r.lo, r.lo + r.n, r.first, r.first + r.m};
