@@ -143,8 +143,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(TileAttention a, Til
             w.all_first = max(w.all_first, __shfl_xor(w.all_first, x));
             w.all_last = min(w.all_last, __shfl_xor(w.all_last, x));
           }
-        } else {                             // the first token sees the first place, the last one the last
+        } else {                             // the first token with a place sees the first one, the last one the last
           add(t0, 0);
+          add(min(t1, max(t0, -w.first)), 0);
           add(t1, 0);
         }
         if (a_hi > 0) w.a_lo = a_lo, w.a_hi = a_hi;

@@ -266,6 +266,75 @@ def test_chunk_attention_values_not_finite_reach_only_rows_that_see_them(eg, fmt
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("D,new", [(64, [7, 3]), (96, [4, 2]), (128, [7, 3]), (256, [7, 3])])
+def test_chunk_attention_of_few_rows_values_not_finite(eg, fmt, D, new):
+    """As above, where all sequences have few rows."""
+    rng, ps = np.random.default_rng(11), 16
+    c = Chunk(eg, rng, fmt, ps, 8, 2, D, new, [150, 70], dict(window=80), spoil=False)
+    before = c.check()
+    nan, inf = (0x7FC1, 0x7F80) if fmt == "bf16" else (0x7F, 0xFF)
+    first = 150 - new[0] - 79                          # the first place that the first token sees
+    touched = np.zeros(sum(new), bool)
+    for place, what in ((149, nan), (147, inf), (first, nan), (first + 2, inf), (first - 1, nan)):
+        c.arrays[1][c.table[0, place // ps], :, place % ps, [5, 17]] = what
+        touched[:new[0]] |= c.seen[0][:, place]
+    c.refresh()
+    c.run()
+    out = c.out.host()
+    assert np.array_equal(c.lse.host(), before[1])
+    value = oracle.bf16_value(out)
+    hit = ~np.isfinite(value)
+    assert np.array_equal(hit.any((1, 2)), touched) and hit[touched].any(1)[:, [5, 17]].all()
+    assert not hit[..., np.setdiff1d(np.arange(D), [5, 17])].any()
+    assert np.array_equal(out[~touched], before[0][~touched])
+    rest = np.setdiff1d(np.arange(D), [5, 17])
+    assert np.array_equal(out[..., rest], before[0][..., rest])
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("mxfp8", 128), ("bf16", 256)])
+@pytest.mark.parametrize("new,length,window", [(10, 5, 2), (300, 200, 3), (300, 299, 40), (90, 1, 7)])
+def test_chunk_attention_of_more_tokens_than_places_in_a_window(eg, fmt, D, new, length, window):
+    """The first tokens have no place and see nothing; those behind them see places that the last ones do not."""
+    rng = np.random.default_rng(12)
+    Chunk(eg, rng, fmt, 16, 4, 2, D, [new], [length], dict(window=window)).check()
+    docs = docs_for([new], [length], 25)
+    Chunk(eg, rng, fmt, 16, 4, 2, D, [new], [length], dict(window=window, doc_starts=docs)).check()
+    Chunk(eg, rng, fmt, 16, 4, 2, D, [new], [length], dict(window=window, prefix_lens=np.array([2]))).check()
+
+
+@pytest.mark.parametrize("fmt,hq,hkv,D", [("bf16", 8, 2, 64), ("mxfp8", 12, 3, 128), ("bf16", 16, 2, 256)])
+@pytest.mark.parametrize("rules", [{}, dict(window=700), dict(cap=4.0)])
+def test_chunk_attention_of_long_and_short_chunks_at_once(eg, fmt, hq, hkv, D, rules):
+    """Some sequences have a prompt's rows, some a single token's over a long context, some none."""
+    rng = np.random.default_rng(13)
+    c = Chunk(eg, rng, fmt, 16, hq, hkv, D, [300, 1, 2, 0, 200, 3, 1, 8, 1], [1500, 2000, 64, 5, 200, 1100, 2900, 8, 1], rules,
+              tail=1)
+    first = c.check()
+    c.ws.t.fill_(255)
+    assert all(np.array_equal(a, b) for a, b in zip(first, c.check()))
+
+
+def test_chunk_attention_graphs_that_share_a_workspace(eg):
+    """Two captured calls of different sizes with one workspace, replayed in turn."""
+    rng = np.random.default_rng(14)
+    calls = [Chunk(eg, rng, "bf16", 16, 8, 2, 128, new, lens) for new, lens in
+             (([200, 30], [2000, 40]), ([1, 1, 4], [900, 3, 1200]))]
+    want = [c.check() for c in calls]
+    ws = max((c.ws for c in calls), key=lambda g: g.t.numel())
+    graphs = []
+    for c in calls:
+        c.ws = ws
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run()
+    for i in (0, 1, 1, 0, 1, 0):
+        calls[i].out.t.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(calls[i].out.host(), want[i][0]) and np.array_equal(calls[i].lse.host(), want[i][1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
 def test_chunk_attention_bad_pages_are_not_seen(eg, fmt):
     rng = np.random.default_rng(9)
     c = Chunk(eg, rng, fmt, 16, 8, 2, 128, [40, 5, 3], [300, 16, 64], spoil=False)
@@ -360,6 +429,16 @@ def test_shared_prefix_attention(eg, fmt, ps, hq, hkv, D, cu, prefixes, lens):
     first = s.check()
     s.ws.t.fill_(255)
     assert all(np.array_equal(a, b) for a, b in zip(first, s.check()))
+
+
+@pytest.mark.parametrize("fmt,hq,hkv,D", [("bf16", 8, 2, 64), ("mxfp8", 40, 1, 128)])
+def test_shared_prefix_attention_of_many_groups(eg, fmt, hq, hkv, D):
+    """Groups of none, one and many sequences, prefixes of all lengths, sequences of no group before and behind them."""
+    rng = np.random.default_rng(22)
+    sizes = np.concatenate([rng.integers(0, 4, size=60), [40]])
+    cu = np.concatenate([[2], 2 + np.cumsum(sizes)])
+    n = int(cu[-1]) + 3
+    Shared(eg, rng, fmt, 16, hq, hkv, D, cu, rng.integers(0, 700, size=61), rng.integers(0, 90, size=n)).check()
 
 
 def test_shared_prefix_attention_lengths_out_of_range_and_bad_pages(eg):
@@ -630,6 +709,24 @@ def test_together_on_another_stream_and_in_a_graph(eg):
         graph.replay()
         got = s.results()
         assert all(np.array_equal(a, b) for a, b in zip(want, got))
+
+
+def test_together_on_two_streams_at_once(eg):
+    runs = [Generation(eg, seed) for seed in (51, 52)]
+    want = []
+    for s in runs:
+        s.run()
+        want.append(s.results())
+    sides = [torch.cuda.Stream() for _ in runs]
+    for s in runs:
+        for t in (s.out, s.lse, s.out1, s.kept):
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, side in zip(runs, sides):
+            s.run(stream=side)
+    for s, w in zip(runs, want):
+        assert all(np.array_equal(a, b) for a, b in zip(w, s.results()))
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
