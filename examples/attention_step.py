@@ -4,11 +4,10 @@
 
 The streams share a paged cache.  A pass takes some tokens of each stream through the
 layer: the Engram forward in place on the highway, a norm, the 4-bit QKV projection, norm
-and rotation of queries and keys, keys and values into the cache, paged attention, and the
-4-bit output projection added to the highway.  The prompts go through it at once, each
-token attending to its stream's places up to its own (as a sequence of one new token each);
-then each decode step takes every stream's next token, the lookback store carrying the ids
-before it.  The decode step is captured into a HIP graph once and replayed.  After the
+and rotation of queries and keys, keys and values into the cache, attention, and the 4-bit
+output projection added to the highway.  The prompts go through it at once, each token
+attending to its stream's places up to its own; then each decode step takes every stream's
+next token, the lookback store carrying the ids before it.  The decode step is captured into a HIP graph once and replayed.  After the
 prompts and after the last step the attention is checked against a plain computation on
 the context read back out of the cache.  Weights, embeddings and token ids are random.
 """
@@ -93,16 +92,17 @@ class Pass:
 
     def __init__(self, m, stream, cu_seqlens, positions):
         T, hc, dim = len(stream), m.spec.hc, m.spec.dim
-        self.m, self.T, self.stream, self.positions = m, T, stream, positions
+        self.m, self.T, self.stream, self.cu, self.positions = m, T, stream, cu_seqlens, positions
         self.cids = zeros(T, dtype=torch.int32)
         self.tokens = eg.Tokens(self.cids, cu_seqlens, lookback=m.history, lookback_live=m.live)
         self.engram_ws = zeros(eg.engram_workspace_bytes(T, 1, m.spec.cols, hc, dim), dtype=torch.uint8)
         self.h = zeros(T, hc, dim, dtype=torch.float32)
         self.qkv, self.q, self.att = zeros(T, WIDTH), zeros(T, Q_HEADS, HEAD_DIM), zeros(T, Q_HEADS, HEAD_DIM)
         self.y, self.lse = zeros(T, dim), zeros(T, Q_HEADS, dtype=torch.float32)
-        self.table = m.table[stream].contiguous()   # a row for each token
-        self.ws = zeros(eg.engram_paged_attention_workspace_bytes(T, Q_HEADS, KV_HEADS, HEAD_DIM, MAX_LEN),
-                        dtype=torch.uint8)
+        self.prompts = T > len(PROMPTS)             # several tokens a stream
+        need = (eg.engram_chunk_attention_workspace_bytes(T, len(PROMPTS), Q_HEADS, KV_HEADS, HEAD_DIM, MAX_LEN) if self.prompts
+                else eg.engram_paged_attention_workspace_bytes(T, Q_HEADS, KV_HEADS, HEAD_DIM, MAX_LEN))
+        self.ws = zeros(need, dtype=torch.uint8)
 
     def run(self):
         m, T, dim = self.m, self.T, self.m.spec.dim
@@ -117,8 +117,12 @@ class Pass:
         slots = m.slot_of[self.stream, self.positions.long()]
         eg.engram_qk_norm_rope(self.qkv, Q_HEADS, KV_HEADS, HEAD_DIM, m.q_weight, m.k_weight, EPS, self.positions,
                                m.inv_freq, False, self.q, cache=m.cache, slots=slots, bad_slots=m.bad)
-        eg.engram_paged_attention(m.cache, self.q, self.table, self.positions + 1, MAX_LEN, SCALE, self.att, self.ws,
-                                  lse=self.lse, bad_pages=m.bad)
+        where = dict(lse=self.lse, bad_pages=m.bad)
+        if self.prompts:
+            lens = self.positions[self.cu[1:].long() - 1] + 1
+            eg.engram_chunk_attention(m.cache, self.q, self.cu, m.table, lens, MAX_LEN, SCALE, self.att, self.ws, **where)
+        else:
+            eg.engram_paged_attention(m.cache, self.q, m.table, self.positions + 1, MAX_LEN, SCALE, self.att, self.ws, **where)
         eg.engram_project_mxfp4(self.att, *m.wo, self.y, T, Q_HEADS * HEAD_DIM, dim)
         self.h.add_(self.y.view(torch.bfloat16).float()[:, None])
 
