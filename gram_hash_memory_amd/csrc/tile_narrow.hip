@@ -8,6 +8,11 @@
 // the next tile requested as soon as a register is free, its pages a tile earlier.
 // At the end of a block, or of a run's piece of one, the waves' results are joined
 // in LDS.
+//
+// 64 single tokens over up to 4095 places in 8 bits with capped scores and a distance
+// bias (338 MB): 78 us, 4.4 TB/s; the cap's and the bias's arithmetic is what keeps it
+// from the copy's rate.  Pages are asked for two tiles ahead because a wait for them
+// was one for the next tile's keys as well (251 us).
 #include "attention_common.hpp"
 #include "tile_plan.hpp"
 
@@ -390,7 +395,8 @@ __device__ __forceinline__ void work_piece(const TileAttention &a, const TilePla
   }
 }
 
-// 32 rows of larger heads than this do not fit the registers.
+// 32 rows of larger heads than this do not fit the registers; of smaller ones they save
+// reading the places twice, which costs 16 rows nothing to leave out.
 constexpr int kMostTwo = 160;
 // Registers for two workgroups a CU where they suffice.
 constexpr int groups_per_cu(int db, int ht) { return db * ht <= 4 ? 2 : 1; }

@@ -3,9 +3,12 @@
 //
 // The host knows neither the tokens of a sequence nor its length, so a kernel of one
 // workgroup a list writes the blocks down.  Where there are enough blocks, the
-// workgroups of the lists' kernels take whole ones off a queue; where there are too
-// few to fill the GPU, equal runs of all tiles, and a third kernel adds the parts of
-// a block in order.
+// workgroups of the lists' kernels take whole ones, those of most tiles first; where
+// there are too few to fill the GPU, equal runs of all tiles, and a third kernel adds
+// the parts of a block in order.  Which, the plan kernel decides.  It takes 7 us, a
+// chain of dependent loads and scans (13 us for 64 blocks with documents, whose starts
+// it reads); the join 5 us for a few blocks, 28 us for 256 rows of each of 256 runs
+// (134 MB read), 13 us for 64 sequences behind a shared prefix.
 #include <algorithm>
 
 #include "attention_common.hpp"
@@ -17,8 +20,14 @@ namespace {
 using namespace attn;
 
 constexpr int kPlanThreads = 1024;
-constexpr int kWholePlaces = 512;          // contexts that are never cut
-constexpr int kWideJoin = 8, kNarrowJoin = 3;      // what cutting costs, in tiles of the list
+// Contexts that are never cut, which saves the join's launch: two single tokens over up
+// to 500 places 23.5 us (cut: 26.5), over up to 900 29.6 us (cut: 25.5).
+constexpr int kWholePlaces = 512;
+// What cutting costs, in tiles of the list.  Wide: three ragged prompts of capped scores
+// 161 us whole and 241 us cut (which 4 would choose), 2048 tokens behind 14336 632 us
+// whole and 690 us cut; from 8 to 40 nothing changes.  Narrow: 64 sequences behind a
+// prefix 71 us with 3, 76 us with 1, the same with 12.
+constexpr int kWideJoin = 8, kNarrowJoin = 3;
 
 inline int64_t ceil_div(int64_t x, int64_t by) { return (x + by - 1) / by; }
 
@@ -325,9 +334,13 @@ Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int
   const int64_t group = q_heads / kv_heads, rows = T * group;
   const int64_t problems = n_groups > 0 ? n_groups : n_seqs;
   TileList &wide = s.list[0], &narrow = s.list[1];
-  // Few rows a problem on the average: all of them in narrow blocks.  Else narrow
-  // blocks for the problems that have no more than one, where there may be several
-  // whose places take long to read (two more launches, some 5 us).
+  // Few rows a problem on the average: all of them in narrow blocks (64 sequences of
+  // 64 rows over up to 4095 places 294 us, in wide blocks 357; of 96 rows 416 against
+  // 368; one of 64 rows over 14336 places 66 against 60).  Else narrow blocks for the
+  // problems that have no more than one, where there may be several whose places take
+  // long to read: 2048 tokens and 63 single ones over up to 4095 places 270 us (all wide:
+  // 370), over up to 1000 174 us (146); 512 tokens and 3 single ones 71 us either way,
+  // 7 single ones over up to 900 62 us (59).  Two more launches are some 5 us.
   const bool all_narrow = rows <= 2 * kRows * problems;
   const bool some_narrow = all_narrow || n_groups > 0 || (n_seqs >= 8 && max_len > 2 * kWholePlaces);
   narrow.block_rows = tile_narrow_rows(head_dim, n_groups > 0 && !all_narrow ? group : ceil_div(rows, problems));
