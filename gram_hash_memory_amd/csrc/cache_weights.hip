@@ -9,8 +9,8 @@
 // writes a place, so the sums do not depend on timing.  No tile passes through shared memory:
 // keys are read once, and the query rows, which all of a head's waves read, come from the L2.
 // Where few rows see a place the reading of the keys bounds it (64 streams of up to 4095
-// places in 8 bits, 180 MB with the weights: 66 us), where many do, the exponential and its
-// bookkeeping, some ten operations a place and row (64 tokens after 16320 places: 31 us).
+// places in 8 bits, 180 MB with the weights: 49 us), where many do, the exponential and its
+// bookkeeping, some ten operations a place and row (64 tokens after 16320 places: 32 us).
 #include "attention_common.hpp"
 #include "tile_plan.hpp"
 
@@ -19,20 +19,21 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWaves = 4;
+// One wave a workgroup: its places are free for the next wave's as soon as it is done (64
+// streams of up to 4095 places: 49 us, with 2, 4, 8 and 16 waves 54, 66, 79 and 89).
+constexpr int kThreads = 64;
 
 // kU: tiles of 16 places that a wave takes; a query row's part of the work, what it sees
 // and its sum, is shared by them.
 template <int kDb, bool kMx, int kU>
-__global__ __launch_bounds__(64 * kWaves, kU == 2 && kDb <= 4 ? 4 : 2) void cache_weights_kernel(CacheWeights a, int chunks) {
+__global__ __launch_bounds__(kThreads, kU == 2 && kDb <= 4 ? 4 : 2) void cache_weights_kernel(CacheWeights a, int chunks) {
   constexpr int D = 32 * kDb, kRowBytes = kMx ? D : 2 * D, kPlaces = 16 * kU;
   constexpr int kWords = kMx ? (kDb + 1) / 2 : kDb;          // of 16 bytes a lane and key
   const CacheView &c = a.cache;
-  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x, col = lane & 15, g = lane >> 4;
   const int64_t pair = blockIdx.x / chunks;
   const int s = int(pair / c.kv_heads), kvh = int(pair - int64_t(s) * c.kv_heads);
-  const int p0 = __builtin_amdgcn_readfirstlane(
-      (int(blockIdx.x - pair * chunks) * kWaves + int(threadIdx.x >> 6)) * kPlaces);
+  const int p0 = int(blockIdx.x - pair * chunks) * kPlaces;
   const int len = length_of(a.lens[s], a.max_len, a.table_width, c.page_shift);
   if (p0 >= len) return;
   const int begin = min(max(a.cu[s], 0), a.T), end = min(max(a.cu[s + 1], begin), a.T);
@@ -210,13 +211,12 @@ __global__ __launch_bounds__(64 * kWaves, kU == 2 && kDb <= 4 ? 4 : 2) void cach
 
 // Few rows a sequence: what counts is how many waves have keys on their way, and 32 places
 // leave registers for 16 of them on a compute unit (64 streams of up to 4095 places in 8 bits,
-// 4 rows a key-value head: 66 us, with 64 places 91).  Many rows: that a row's part is shared
-// (64 tokens after 16320 places, 256 rows a head: 31 us, with 32 places 41).
+// 4 rows a key-value head, in workgroups of 4 waves: 66 us, with 64 places 91).  Many rows: that a row's part is shared
+// (64 tokens after 16320 places, 256 rows a head: 31 us, with 32 places 41, in workgroups of 4).
 constexpr int tiles_of(int db, bool few) { return few || db > 4 ? 2 : 4; }
 bool few_rows(int32_t T, int32_t n_seqs, int32_t group) { return int64_t(T) * group <= 32 * int64_t(n_seqs); }
 int64_t chunks_of(int32_t max_len, int tiles) {
-  const int64_t places = int64_t(kWaves) * 16 * tiles;
-  return (max_len + places - 1) / places;
+  return (max_len + int64_t(16) * tiles - 1) / (16 * tiles);
 }
 
 template <int kDb, bool kFew>
@@ -224,10 +224,10 @@ hipError_t launch(const CacheWeights &a, hipStream_t stream) {
   constexpr int kU = tiles_of(kDb, kFew);
   const int64_t chunks = chunks_of(a.max_len, kU), blocks = int64_t(a.n_seqs) * a.cache.kv_heads * chunks;
   if (a.cache.k_scales)
-    hipLaunchKernelGGL((cache_weights_kernel<kDb, true, kU>), dim3(unsigned(blocks)), dim3(64 * kWaves), 0, stream, a,
+    hipLaunchKernelGGL((cache_weights_kernel<kDb, true, kU>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, a,
                        int(chunks));
   else
-    hipLaunchKernelGGL((cache_weights_kernel<kDb, false, kU>), dim3(unsigned(blocks)), dim3(64 * kWaves), 0, stream, a,
+    hipLaunchKernelGGL((cache_weights_kernel<kDb, false, kU>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, a,
                        int(chunks));
   return hipGetLastError();
 }
@@ -240,7 +240,7 @@ hipError_t by_rows(const CacheWeights &a, hipStream_t stream) {
 }  // namespace
 
 int64_t cache_weights_blocks(int32_t n_seqs, int32_t kv_heads, int32_t max_len) {
-  return int64_t(n_seqs) * kv_heads * chunks_of(max_len, 2);
+  return (int64_t(n_seqs) * kv_heads * chunks_of(max_len, 2) + 3) / 4;
 }
 
 hipError_t launch_cache_weights(const CacheWeights &a, hipStream_t stream) {

@@ -637,9 +637,13 @@ ENGRAM_API size_t engram_chunk_attention_workspace_bytes(int32_t T, int32_t n_se
  *   rows that do not see it, whatever it holds.  Scores, softmax statistics and
  *   sums are held in fp32; a weight exp(.) is rounded to bf16 for the matrix cores.
  *   Results do not depend on timing.
- *   Limits: T and max_len at most 2^30; with B blocks of 128 rows (T * q_heads /
- *   kv_heads / 128 + n_seqs), B * (max_len / 64 + 2) * kv_heads below 2^28.
- *   workspace DEVICE, 256-byte aligned; its contents are scratch.
+ *   out and lse must not overlap the inputs.
+ *   Limits: T, n_seqs, max_len and the rows T * q_heads / kv_heads at most 2^30;
+ *   with B = rows / 128 + n_seqs blocks, or rows / 16 + n_seqs where a sequence has
+ *   at most 64 rows on the average, B * kv_heads * (max_len / 64 + 3) below 2^31.
+ *   Beyond them the call returns ENGRAM_ERR_UNSUPPORTED.
+ *   workspace DEVICE, 256-byte aligned; its contents are scratch.  Calls that may
+ *   overlap in time need one each.
  */
 ENGRAM_API engram_status engram_chunk_attention(
     const engram_kv_cache *cache, const uint16_t *q, int32_t T, const int32_t *cu_seqlens,
@@ -663,8 +667,9 @@ ENGRAM_API size_t engram_shared_prefix_attention_workspace_bytes(
  *   engram_paged_attention; results are those of that call over the prefix's
  *   places followed by the own ones (weights are rounded as in
  *   engram_chunk_attention).  n_groups >= 1.
- *   Limits as for engram_chunk_attention, with T = n_seqs and n_groups + n_seqs
- *   more blocks, and n_seqs * q_heads below 2^30.
+ *   Limits as for engram_chunk_attention, with T = n_seqs, n_groups for its n_seqs,
+ *   the larger of max_prefix and max_len, and ceil(q_heads / kv_heads / 16) more
+ *   blocks a sequence; n_seqs * q_heads below 2^30 and B * kv_heads * 8 below 2^24.
  */
 ENGRAM_API engram_status engram_shared_prefix_attention(
     const engram_kv_cache *cache, const uint16_t *q, const int32_t *cu_groups,
@@ -705,6 +710,8 @@ ENGRAM_API engram_status engram_cache_weights(
  *   DEVICE fp32 [n_seqs][kv_heads][new_weights_stride], new_weights_stride >= keep:
  *   the kept places' weights, then 0; kept DEVICE int32 [n_seqs][kv_heads][keep]:
  *   the kept places, then -1.  Outputs must not overlap the inputs.
+ *   What is kept is renumbered: a later call's windows and distances count the new
+ *   places.
  *   A kept place on a page outside the cache becomes zeros, one that goes to such a
  *   page is not written; bad_pages (nullable) is incremented at least once for
  *   either.
