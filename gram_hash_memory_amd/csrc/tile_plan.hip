@@ -10,6 +10,7 @@
 // it reads); the join 5 us for a few blocks, 28 us for 256 rows of each of 256 runs
 // (134 MB read), 13 us for 64 sequences behind a shared prefix.
 #include <algorithm>
+#include <cstdint>
 
 #include "attention_common.hpp"
 #include "tile_plan.hpp"
@@ -368,8 +369,9 @@ Sizes sizes_of(int32_t T, int32_t n_seqs, int32_t n_groups, int32_t q_heads, int
 
 inline int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Lays the plan out from `base` on; returns its bytes.
-int64_t lay_out(const Sizes &s, int64_t problems, int64_t head_dim, uint8_t *base, TilePlan *plan) {
+// Lays the plan out from `workspace` on; returns its bytes.
+int64_t lay_out(const Sizes &s, int64_t problems, int64_t head_dim, void *workspace, TilePlan *plan) {
+  const uintptr_t base = reinterpret_cast<uintptr_t>(workspace);      // null for the bytes alone
   int64_t at = 256;
   for (int i = 0; i < 2; ++i) {
     TileList l = s.list[i];
@@ -418,7 +420,7 @@ hipError_t launch_tile_attention(const TileAttention &a, hipStream_t stream) {
   const int D = a.cache.head_dim, hkv = a.cache.kv_heads;
   const Sizes s = sizes_of(a.T, a.n_seqs, a.n_groups, a.q_heads, hkv, D, a.max_len, a.max_prefix);
   TilePlan plan{};
-  lay_out(s, a.n_groups + int64_t(a.n_seqs), D, static_cast<uint8_t *>(a.workspace), &plan);
+  lay_out(s, a.n_groups + int64_t(a.n_seqs), D, a.workspace, &plan);
   hipLaunchKernelGGL(plan_kernel, dim3(2), dim3(kPlanThreads), 0, stream, a, plan);
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && plan.list[0].max_blocks > 0) err = launch_tile_wide(a, plan, stream);
